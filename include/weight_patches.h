@@ -111,7 +111,10 @@ typedef struct wp_adapter {
 
 /* Operation ids for lora_workspace_size(). */
 enum { WP_OP_FWD = 0, WP_OP_FWD_GROUPED = 1, WP_OP_BWD = 2, WP_OP_FWD_HOST = 3, WP_OP_SWIGLU_FWD = 4, WP_OP_MERGE = 5,
-       WP_OP_FWD_EXACT = 6 };
+       WP_OP_FWD_EXACT = 6, WP_OP_NORM_BWD = 7 };
+
+/* Norm kinds: layer norm (mean taken out) and the form without a mean (RMS norm). */
+enum { WP_NORM_LAYER = 0, WP_NORM_RMS = 1 };
 
 /*
  * lora_linear_fwd -- Y = X W^T + bias + sum_p s_p (X A_p^T) B_p^T.
@@ -372,6 +375,148 @@ int lora_linear_fwd_exact(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
 int lora_linear_fwd_noalloc(const wp_mat* X, const wp_mat* W, const wp_mat* bias,
                             const wp_adapter* adapters, int32_t n_adapters, double request_scale,
                             const wp_out* Y, void* stream);
+
+/* ------------------------------------------------------------ adapters of many requests
+ * A bank holds the adapters of one layer, one per slot, each padded to the bank's rank with
+ * zero rows of A (zero columns of B):
+ *   A [n_slots, n_groups * rank, in]   group g's rows g * rank .. (g + 1) * rank - 1
+ *   B [n_slots, out, rank]             out = n_groups * out_g stacked output rows
+ * both WP_BF16, contiguous, 16-byte aligned; scale [n_slots] fp32 (alpha / r * strength of
+ * each adapter), all on the device.  rank % 8 == 0, 8 <= rank <= 256. */
+typedef struct wp_bank {
+  const void* A;
+  const void* B;
+  const float* scale;
+  int32_t dtype;
+  int32_t n_slots, n_groups, rank;
+  int64_t in, out;
+} wp_bank;
+
+/*
+ * lora_linear_fwd_multi -- one shared projection for rows that belong to the requests of many
+ * adapters (sglang PR, Motivation: the adapter and its scale belong to the request):
+ *   Y[t, g] = X[t] W_g^T + bias_g + s_t (X[t] A_{a,g}^T) B_{a,g}^T,   a = slot[t],
+ *   s_t = scale[a] * row_scale[t] * request_scale
+ * (products of fp32, rounded one after another), per column group g of bank->n_groups.
+ *   X        [T, in] WP_BF16.
+ *   W        [out, in] WP_BF16 or WP_NF4, or NULL (the adapters' term alone).
+ *   bias     [out] WP_BF16 or WP_FP32, or NULL.
+ *   slot     [T] int32 on the device, in any order; a value outside 0 .. n_slots - 1 (-1 by
+ *            convention) means that the row uses no adapter.  The values may change between
+ *            replays of a captured graph.
+ *   row_scale [T] fp32 on the device or NULL (1): the scale of each row's request.
+ *   Y        [T, out] WP_BF16 or WP_FP32; must not overlap the inputs.
+ * A row's result depends on that row and its adapter alone: a row without an adapter, or whose
+ * s_t is exactly 0, equals the row of the plain projection, and values that are not finite in
+ * one slot or row do not reach rows of other slots.  As in lora_linear_fwd, s X A^T is rounded
+ * once to bf16, sums are fp32 and the output is rounded once.
+ *   workspace: lora_multi_workspace_size(X, W, bank) bytes, 16-byte aligned.
+ * Alignment: as lora_linear_fwd's tensor-core path (16-byte bases and pitches, in % 8 == 0,
+ * out_g % 8 == 0); n_groups <= 8.  Errors as lora_linear_fwd; WP_ERR_DTYPE for a bank that is
+ * not bf16, WP_ERR_UNSUPPORTED for a rank above 256.
+ */
+int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, const wp_bank* bank,
+                          const int32_t* slot, const float* row_scale, double request_scale,
+                          const wp_out* Y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace that lora_linear_fwd_multi needs (0: a rejected shape). */
+size_t lora_multi_workspace_size(const wp_mat* X, const wp_mat* W, const wp_bank* bank);
+
+/* ------------------------------------------------------------------------- norms
+ * lora_norm_fwd -- y = (x - mu) r w + b over the rows of X, r = 1 / sqrt(var + eps)
+ *   WP_NORM_LAYER: mu the row's mean, var its mean squared distance from mu;
+ *   WP_NORM_RMS:   mu = 0, var the mean square.
+ * (FastVideo API docs, DenseLoRAPatch: .diff / .diff_b payloads on norm vectors; this is the
+ *  layer those vectors belong to, and lora_norm_bwd gives the gradients that train them.)
+ *   X [T, C] WP_BF16 or WP_FP32, any row pitch; weight, bias [C] WP_BF16 or WP_FP32 or NULL
+ *   (1 and 0); Y [T, C] of X's dtype.
+ *   stats [2, T] fp32 or NULL: the rows' mu and r, for the backward.
+ * Sums are fp32, the mean taken out before squaring; one output rounding.  eps >= 0, finite.
+ */
+int lora_norm_fwd(const wp_mat* X, const wp_mat* weight, const wp_mat* bias, int32_t kind, double eps,
+                  const wp_out* Y, float* stats, void* stream);
+
+/*
+ * lora_norm_bwd -- with xh = (x - mu) r and h = dy w:
+ *   dx = r (h - mean(h) - xh mean(h xh))      (WP_NORM_RMS: without mean(h))
+ *   dw = sum over rows of dy xh,   db = sum over rows of dy.
+ *   dY, X [T, C] of one dtype (WP_BF16 or WP_FP32); stats [2, T] as lora_norm_fwd wrote them;
+ *   dX [T, C] of X's dtype or NULL; dW, dB [1, C] WP_FP32 or NULL, overwritten (zero for no
+ *   rows).  weight NULL: 1.
+ *   workspace: lora_workspace_size(WP_OP_NORM_BWD, X, NULL, NULL, 0) bytes when dW or dB is
+ *   asked for.  Row sums are added in a fixed order: the same call gives the same bits.
+ */
+int lora_norm_bwd(const wp_mat* dY, const wp_mat* X, const wp_mat* weight, const float* stats, int32_t kind,
+                  const wp_out* dX, const wp_out* dW, const wp_out* dB, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- AdamW
+ * One tensor of an adapter set.  param [numel] WP_BF16 or WP_FP32; master [numel] fp32 or NULL:
+ * when given (with a bf16 param) the step updates the master and param is its rounding.
+ * state_bits 32: m, v [numel] fp32.  state_bits 8: m [numel] int8 codes, v [numel] uint8 codes
+ * and one fp32 scale per 256 consecutive elements (m_absmax, v_absmax [ceil(numel / 256)]): a
+ * code q of a block of scale a stands for
+ *     m: a sign(q) (|q| / 127)^2,      v: a (q / 255)^4,
+ * the nearest code in the root's domain, a v above zero never coded as zero.  Zeroed codes and
+ * scales are the initial state. */
+typedef struct wp_adamw_tensor {
+  void* param;
+  float* master;
+  void* m;
+  void* v;
+  float* m_absmax;
+  float* v_absmax;
+  int64_t numel;
+  int32_t param_dtype;
+  int32_t state_bits;
+} wp_adamw_tensor;
+
+/* A prepared set: filled by lora_adamw_plan; `table` is the caller's device memory. */
+enum { WP_ADAMW_MAX_LAUNCHES = 16, WP_ADAMW_TENSORS_PER_LAUNCH = 3900 };
+typedef struct wp_adamw_plan {
+  void* table;
+  int32_t n_tensors;
+  int32_t n_launches;
+  int64_t unit_begin[WP_ADAMW_MAX_LAUNCHES + 1];
+} wp_adamw_plan;
+
+/* The step's scalars.  g = grad * grad_scale (* grad_scale_dev[0] when not NULL: a clip or loss
+ * scale formed on the device); step counts from 1. */
+typedef struct wp_adamw_args {
+  double lr, beta1, beta2, eps, weight_decay, grad_scale;
+  int64_t step;
+  const float* grad_scale_dev;
+} wp_adamw_args;
+
+/* Device bytes of a set's table (0 for a rejected list). */
+size_t lora_adamw_plan_size(const wp_adamw_tensor* tensors, int32_t n);
+
+/* Writes the set's table into `table` (16-byte aligned device memory of lora_adamw_plan_size
+ * bytes, which has to live as long as the plan is used) with small kernels on `stream`, and
+ * fills *plan.  At most 62400 tensors; every pointer aligned to its element type. */
+int lora_adamw_plan_init(const wp_adamw_tensor* tensors, int32_t n, void* table, size_t table_bytes,
+                         wp_adamw_plan* plan, void* stream);
+
+/*
+ * lora_adamw_step -- one AdamW step (decoupled weight decay) over the whole set, in place:
+ *     m <- b1 m + (1 - b1) g,   v <- b2 v + (1 - b2) g^2
+ *     p <- p (1 - lr wd) - lr / (1 - b1^step) * m / (sqrt(v) / sqrt(1 - b2^step) + eps)
+ * (the dA, dB of lora_linear_bwd and dW, dB of lora_norm_bwd are its gradients).  The scalars are
+ * formed in double and rounded once to fp32; moments and parameters are fp32 while they are
+ * updated (8-bit moments are coded again after p has used them), each product and sum of m and v
+ * a separate rounding.  A gradient that is not finite reaches its element's p, m and v, and every
+ * value of its 8-bit block.
+ *   grads: host array of n_tensors device pointers, all of grad_dtype (WP_FP32 or WP_BF16); NULL
+ *   leaves that tensor and its state untouched.  Read before the call returns.
+ * Errors: WP_ERR_INVALID for a scalar that is not finite, betas outside [0, 1), eps < 0, step < 1.
+ */
+int lora_adamw_step(const wp_adamw_plan* plan, const void* const* grads, int32_t grad_dtype,
+                    const wp_adamw_args* args, void* stream);
+
+/* The fp32 values of 8-bit moments: codes [numel] (int8 when is_signed, else uint8), absmax
+ * [ceil(numel / 256)], out [numel]. */
+int lora_block8_decode(const void* codes, int32_t is_signed, const float* absmax, int64_t numel, float* out,
+                       void* stream);
 
 /* Bytes of device workspace the given call needs (0 if none).  `op` is WP_OP_*;
  * the other arguments are those of the call (adapters: n_adapters, or n_groups). */

@@ -12,6 +12,9 @@ Entry points (same names as the C ABI):
     lora_linear_bwd          closed-form dX, dA, dB
     lora_linear_fwd_exact    the unfused bf16 chain (the "exact" tier), unit scales skipped or not
     lora_dense_patch         .diff / .diff_b (add) and .set_weight (replace), in place
+    lora_linear_fwd_multi    one projection for rows of many adapters (an AdapterBank)
+    lora_norm_fwd / _bwd     layer norm or RMS norm, and the gradients of x, weight, bias
+    lora_adamw_plan / _step  one AdamW step over many tensors, 32- or 8-bit moments
 """
 from __future__ import annotations
 
@@ -27,7 +30,8 @@ LIB_PATH = os.path.join(_HERE, "libweight_patches_gb300.so")
 
 WP_BF16, WP_FP32, WP_NF4 = 0, 1, 2
 WP_PATCH_ADD, WP_PATCH_SET = 0, 1
-WP_OP_FWD, WP_OP_FWD_GROUPED, WP_OP_BWD, WP_OP_FWD_HOST, WP_OP_SWIGLU_FWD, WP_OP_MERGE, WP_OP_FWD_EXACT = range(7)
+WP_OP_FWD, WP_OP_FWD_GROUPED, WP_OP_BWD, WP_OP_FWD_HOST, WP_OP_SWIGLU_FWD, WP_OP_MERGE, WP_OP_FWD_EXACT, WP_OP_NORM_BWD = range(8)
+WP_NORM_LAYER, WP_NORM_RMS = 0, 1
 STATUS = {0: "WP_OK", -1: "WP_ERR_INVALID", -2: "WP_ERR_SHAPE", -3: "WP_ERR_DTYPE",
           -4: "WP_ERR_ALIGN", -5: "WP_ERR_WORKSPACE", -6: "WP_ERR_CUDA", -7: "WP_ERR_TIMEOUT",
           -8: "WP_ERR_UNSUPPORTED"}
@@ -46,6 +50,29 @@ class WpOut(ctypes.Structure):
 class WpAdapter(ctypes.Structure):
     _fields_ = [("A", WpMat), ("B", WpMat), ("alpha", ctypes.c_double),
                 ("strength", ctypes.c_double), ("bias_B", ctypes.c_void_p), ("bias_B_dtype", ctypes.c_int32)]
+
+
+class WpBank(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("n_slots", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("in_", ctypes.c_int64), ("out", ctypes.c_int64)]
+
+
+class WpAdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_absmax", ctypes.c_void_p), ("v_absmax", ctypes.c_void_p),
+                ("numel", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32)]
+
+
+class WpAdamWPlan(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_tensors", ctypes.c_int32), ("n_launches", ctypes.c_int32),
+                ("unit_begin", ctypes.c_int64 * 17)]
+
+
+class WpAdamWArgs(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("step", ctypes.c_int64), ("grad_scale_dev", ctypes.c_void_p)]
 
 
 class WeightPatchesError(RuntimeError):
@@ -82,6 +109,18 @@ def _load():
     lib.lora_merge_seeded.argtypes = [pm, po, pa, I32, D, ctypes.c_uint64, P, SZ, P]
     lib.lora_swiglu_bwd.argtypes = [pm, pm, po, po, P]
     lib.lora_dense_patch.argtypes = [P, I32, I64, P, I32, I64, I32, D, P]
+    pb = ctypes.POINTER(WpBank)
+    pt, pp, pg = ctypes.POINTER(WpAdamWTensor), ctypes.POINTER(WpAdamWPlan), ctypes.POINTER(WpAdamWArgs)
+    lib.lora_linear_fwd_multi.argtypes = [pm, pm, pm, pb, P, P, D, po, P, SZ, P]
+    lib.lora_multi_workspace_size.argtypes = [pm, pm, pb]
+    lib.lora_multi_workspace_size.restype = SZ
+    lib.lora_norm_fwd.argtypes = [pm, pm, pm, I32, D, po, P, P]
+    lib.lora_norm_bwd.argtypes = [pm, pm, pm, P, I32, po, po, po, P, SZ, P]
+    lib.lora_adamw_plan_size.argtypes = [pt, I32]
+    lib.lora_adamw_plan_size.restype = SZ
+    lib.lora_adamw_plan_init.argtypes = [pt, I32, P, SZ, pp, P]
+    lib.lora_adamw_step.argtypes = [pp, ctypes.POINTER(P), I32, pg, P]
+    lib.lora_block8_decode.argtypes = [P, I32, P, I64, P, P]
     lib.lora_workspace_size.argtypes = [I32, pm, pm, pa, I32]
     lib.lora_workspace_size.restype = SZ
     lib.lora_status_string.argtypes = [ctypes.c_int]
@@ -94,7 +133,9 @@ def _load():
     lib.lora_last_cuda_error.restype = ctypes.c_char_p
     for name in ("lora_linear_fwd", "lora_linear_fwd_grouped", "lora_linear_bwd", "lora_dense_patch",
                  "lora_device_status", "lora_linear_fwd_noalloc", "lora_linear_fwd_host",
-                 "lora_linear_fwd_exact", "lora_set_wait_limit", "lora_debug_hold_flags"):
+                 "lora_linear_fwd_exact", "lora_set_wait_limit", "lora_debug_hold_flags",
+                 "lora_linear_fwd_multi", "lora_norm_fwd", "lora_norm_bwd", "lora_adamw_plan_init",
+                 "lora_adamw_step", "lora_block8_decode"):
         getattr(lib, name).restype = ctypes.c_int
     _LIB = lib
     return lib
@@ -377,6 +418,225 @@ def lora_dense_patch(param: torch.Tensor, payload: torch.Tensor, kind: int, stre
                                   _stream(param.device))
     _check(st, "lora_dense_patch")
     return param
+
+
+# ------------------------------------------------------------------- adapters of many requests
+class AdapterBank:
+    """The adapters of one layer, one per slot, each padded with zeros to one rank:
+    ``A`` [slots, n_groups * rank, in] and ``B`` [slots, out, rank] bf16, ``scale`` [slots] fp32
+    (alpha / r * strength of each adapter), all contiguous on one device.  The tensors may be
+    rewritten in place (an adapter loaded into its slot) between calls."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, n_groups: int = 1):
+        if A.dim() != 3 or B.dim() != 3 or scale.dim() != 1:
+            raise ValueError("AdapterBank: A [slots, groups * rank, in], B [slots, out, rank], scale [slots]")
+        if not (A.is_contiguous() and B.is_contiguous() and scale.is_contiguous()):
+            raise ValueError("AdapterBank tensors must be contiguous")
+        if A.dtype not in _DT or B.dtype != A.dtype or scale.dtype != torch.float32:
+            raise ValueError("AdapterBank: A and B of one dtype, scale float32")
+        if not (A.shape[0] == B.shape[0] == scale.shape[0] and A.shape[1] == n_groups * B.shape[2]):
+            raise ValueError("AdapterBank: the shapes of A, B and scale disagree")
+        if not A.device == B.device == scale.device:
+            raise ValueError("AdapterBank tensors must be on one device")
+        self.A, self.B, self.scale, self.n_groups = A, B, scale, n_groups
+        self._c = WpBank(A.data_ptr(), B.data_ptr(), scale.data_ptr(), _DT[A.dtype], A.shape[0], n_groups,
+                         B.shape[2], A.shape[2], B.shape[1])
+
+    @property
+    def out_features(self) -> int:
+        return self.B.shape[1]
+
+
+def lora_multi_workspace_size(X: torch.Tensor, W, bank: AdapterBank) -> int:
+    return _load().lora_multi_workspace_size(_ref(_mat(X)), _ref(_mat(W)), ctypes.byref(bank._c))
+
+
+def lora_linear_fwd_multi(X: torch.Tensor, W, bias: Optional[torch.Tensor], bank: AdapterBank, slot: torch.Tensor,
+                          row_scale: Optional[torch.Tensor] = None, request_scale: float = 1.0,
+                          out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                          workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y[t] = X[t] W^T + bias + s_t (X[t] A_a^T) B_a^T with a = slot[t] (int32; a value outside the
+    bank, -1 by convention, uses no adapter) and s_t = bank.scale[a] * row_scale[t] * request_scale;
+    with ``bank.n_groups`` > 1, per stacked column group.  W bf16, ``NF4Weight`` or None."""
+    T = X.shape[0]
+    if slot.dtype != torch.int32 or slot.numel() != T or not slot.is_contiguous():
+        raise ValueError("slot must be a contiguous int32 tensor with one entry per row of X")
+    if row_scale is not None and (row_scale.dtype != torch.float32 or row_scale.numel() != T
+                                  or not row_scale.is_contiguous()):
+        raise ValueError("row_scale must be a contiguous float32 tensor with one entry per row of X")
+    if out is None:
+        out = torch.empty(T, bank._c.out, dtype=out_dtype, device=X.device)
+    lib, bank_c = _load(), ctypes.byref(bank._c)
+    xm, wm, bm, ym = _mat(X), _ref(_mat(W)), _ref(_mat(bias)), _out(out)
+    if workspace is None:
+        need = lib.lora_multi_workspace_size(ctypes.byref(xm), wm, bank_c)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
+    st = lib.lora_linear_fwd_multi(ctypes.byref(xm), wm, bm, bank_c, slot.data_ptr(),
+                                   None if row_scale is None else row_scale.data_ptr(), request_scale,
+                                   ctypes.byref(ym), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream(X.device))
+    _check(st, "lora_linear_fwd_multi")
+    return out
+
+
+# ----------------------------------------------------------------------------------- norms
+def lora_norm_fwd(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  eps: float = 1e-5, kind: int = WP_NORM_LAYER, out: Optional[torch.Tensor] = None,
+                  stats: Optional[torch.Tensor] = None):
+    """y = (x - mu) r w + b over the rows of X [T, C] (kind ``WP_NORM_RMS``: mu = 0).  Returns
+    (y, stats), stats [2, T] fp32 holding mu and r for ``lora_norm_bwd``."""
+    if out is None:
+        out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    if stats is None:
+        stats = torch.empty(2, X.shape[0], dtype=torch.float32, device=X.device)
+    _check_stats(stats, X.shape[0])
+    st = _load().lora_norm_fwd(ctypes.byref(_mat(X)), _ref(_vec(weight)), _ref(_vec(bias)), kind, eps,
+                               ctypes.byref(_out(out)), stats.data_ptr(), _stream(X.device))
+    _check(st, "lora_norm_fwd")
+    return out, stats
+
+
+def lora_norm_bwd_workspace_size(X: torch.Tensor) -> int:
+    return _load().lora_workspace_size(WP_OP_NORM_BWD, _ref(_mat(X)), None, None, 0)
+
+
+def lora_norm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: Optional[torch.Tensor], stats: torch.Tensor,
+                  kind: int = WP_NORM_LAYER, need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
+                  workspace: Optional[torch.Tensor] = None):
+    """(dX, dW, dB) of ``lora_norm_fwd`` from its stats; dW and dB fp32 [C], None where not asked for."""
+    _check_stats(stats, X.shape[0])
+    T, C = X.shape
+    dx = torch.empty(T, C, dtype=X.dtype, device=X.device) if need_dx else None
+    dw = torch.empty(C, dtype=torch.float32, device=X.device) if need_dw else None
+    db = torch.empty(C, dtype=torch.float32, device=X.device) if need_db else None
+    xm = _mat(X)
+    vec = lambda t: None if t is None else ctypes.byref(WpOut(t.data_ptr(), WP_FP32, 1, C, C))  # noqa: E731
+    if workspace is None and (need_dw or need_db):
+        need = _load().lora_workspace_size(WP_OP_NORM_BWD, ctypes.byref(xm), None, None, 0)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
+    st = _load().lora_norm_bwd(ctypes.byref(_mat(dY)), ctypes.byref(xm), _ref(_vec(weight)), stats.data_ptr(), kind,
+                               None if dx is None else ctypes.byref(_out(dx)), vec(dw), vec(db),
+                               None if workspace is None else workspace.data_ptr(),
+                               0 if workspace is None else workspace.numel() * workspace.element_size(),
+                               _stream(X.device))
+    _check(st, "lora_norm_bwd")
+    return dx, dw, db
+
+
+def _vec(t: Optional[torch.Tensor]) -> Optional[WpMat]:
+    if t is not None and (t.dim() != 1 or not t.is_contiguous()):
+        raise ValueError("weight and bias of a norm must be contiguous vectors")
+    return _mat(t)
+
+
+def _check_stats(stats: torch.Tensor, T: int):
+    if stats.dtype != torch.float32 or stats.numel() != 2 * T or not stats.is_contiguous():
+        raise ValueError("stats must be a contiguous float32 tensor [2, T]")
+
+
+# ----------------------------------------------------------------------------------- AdamW
+@dataclass
+class Block8:
+    """8-bit moments of one tensor: ``codes`` int8 (first moment) or uint8 (second), flat, and
+    ``absmax`` fp32, one per 256 elements.  Zeros are the initial state."""
+
+    codes: torch.Tensor
+    absmax: torch.Tensor
+
+    @staticmethod
+    def zeros(numel: int, signed: bool, device) -> "Block8":
+        return Block8(torch.zeros(numel, dtype=torch.int8 if signed else torch.uint8, device=device),
+                      torch.zeros((numel + 255) // 256, dtype=torch.float32, device=device))
+
+
+class AdamWPlan:
+    """A prepared set of tensors (``lora_adamw_plan``); keeps the tensors and the device table."""
+
+    def __init__(self, c: WpAdamWPlan, table: torch.Tensor, tensors, numels):
+        self._c, self._table, self._tensors, self._numels = c, table, tensors, numels
+        self._ptrs = (ctypes.c_void_p * len(numels))()
+
+
+def lora_adamw_plan(params: Sequence[torch.Tensor], m: Sequence, v: Sequence,
+                    masters: Optional[Sequence[Optional[torch.Tensor]]] = None) -> AdamWPlan:
+    """Prepare ``lora_adamw_step`` over ``params`` (bf16 or fp32, contiguous), their moments (fp32
+    tensors, or ``Block8``) and, for bf16 parameters, optional fp32 masters that the step updates in
+    their place.  The plan refers to these tensors' memory: build it again when one is replaced."""
+    n = len(params)
+    masters = list(masters) if masters is not None else [None] * n
+    if not (n > 0 and n == len(m) == len(v) == len(masters)):
+        raise ValueError("lora_adamw_plan: params, m, v and masters must be lists of one length")
+    arr = (WpAdamWTensor * n)()
+    device = params[0].device
+    for i, (p, mi, vi, ma) in enumerate(zip(params, m, v, masters)):
+        numel, eight = p.numel(), isinstance(mi, Block8)
+        if isinstance(vi, Block8) != eight:
+            raise ValueError("lora_adamw_plan: m and v of one tensor are held alike")
+        if eight:
+            parts = [(mi.codes, torch.int8, numel), (vi.codes, torch.uint8, numel),
+                     (mi.absmax, torch.float32, (numel + 255) // 256), (vi.absmax, torch.float32, (numel + 255) // 256)]
+        else:
+            parts = [(mi, torch.float32, numel), (vi, torch.float32, numel)]
+        if ma is not None:
+            parts.append((ma, torch.float32, numel))
+        for t, dt, count in parts:
+            if t.dtype != dt or t.numel() != count or not t.is_contiguous() or t.device != device:
+                raise ValueError(f"lora_adamw_plan: tensor {i}: a state of the wrong dtype, size, layout or device")
+        if p.dtype not in _DT or not p.is_contiguous() or p.device != device:
+            raise ValueError(f"lora_adamw_plan: parameter {i} must be contiguous bf16 or fp32 on {device}")
+        arr[i] = WpAdamWTensor(p.data_ptr(), None if ma is None else ma.data_ptr(), parts[0][0].data_ptr(),
+                               parts[1][0].data_ptr(), parts[2][0].data_ptr() if eight else None,
+                               parts[3][0].data_ptr() if eight else None, numel, _DT[p.dtype], 8 if eight else 32)
+    lib = _load()
+    table = torch.empty(max(1, lib.lora_adamw_plan_size(arr, n)), dtype=torch.uint8, device=device)
+    c = WpAdamWPlan()
+    _check(lib.lora_adamw_plan_init(arr, n, table.data_ptr(), table.numel(), ctypes.byref(c), _stream(device)),
+           "lora_adamw_plan")
+    return AdamWPlan(c, table, (list(params), list(m), list(v), masters), [p.numel() for p in params])
+
+
+def lora_adamw_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor]], lr: float, beta1: float = 0.9,
+                    beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01, step: int = 1,
+                    grad_scale: float = 1.0, grad_scale_tensor: Optional[torch.Tensor] = None) -> None:
+    """One AdamW step, in place, over the plan's tensors.  ``grads``: one per tensor, contiguous, all
+    fp32 or all bf16; None leaves its tensor untouched.  ``grad_scale_tensor``: a device fp32 scalar
+    that multiplies the gradients as well (a clip or loss scale)."""
+    if len(grads) != len(plan._numels):
+        raise ValueError("lora_adamw_step: one gradient (or None) per tensor")
+    dtype, ptrs = None, plan._ptrs
+    for i, (g, numel) in enumerate(zip(grads, plan._numels)):
+        if g is None:
+            ptrs[i] = None
+            continue
+        if dtype is None:
+            dtype = g.dtype
+        if g.dtype != dtype or g.numel() != numel or not g.is_contiguous():
+            raise ValueError(f"lora_adamw_step: gradient {i} has another dtype, size or layout")
+        ptrs[i] = g.data_ptr()
+    if dtype is None:
+        return
+    if dtype not in _DT:
+        raise ValueError("lora_adamw_step: gradients must be fp32 or bf16")
+    if grad_scale_tensor is not None and (grad_scale_tensor.dtype != torch.float32 or grad_scale_tensor.numel() != 1):
+        raise ValueError("grad_scale_tensor must be one float32 value")
+    args = WpAdamWArgs(lr, beta1, beta2, eps, weight_decay, grad_scale, step,
+                       None if grad_scale_tensor is None else grad_scale_tensor.data_ptr())
+    _check(_load().lora_adamw_step(ctypes.byref(plan._c), ptrs, _DT[dtype], ctypes.byref(args),
+                                   _stream(plan._table.device)), "lora_adamw_step")
+
+
+def lora_block8_decode(codes: torch.Tensor, absmax: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The fp32 values of 8-bit moments (int8 codes: first moments; uint8: second moments)."""
+    if codes.dtype not in (torch.int8, torch.uint8) or not codes.is_contiguous() or not absmax.is_contiguous() \
+            or absmax.dtype != torch.float32 or absmax.numel() != (codes.numel() + 255) // 256:
+        raise ValueError("lora_block8_decode: contiguous int8 or uint8 codes and one fp32 scale per 256 of them")
+    if out is None:
+        out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
+    elif out.dtype != torch.float32 or out.numel() != codes.numel() or not out.is_contiguous():
+        raise ValueError("lora_block8_decode: out must be contiguous fp32 of the codes' size")
+    _check(_load().lora_block8_decode(codes.data_ptr(), codes.dtype == torch.int8, absmax.data_ptr(), codes.numel(),
+                                      out.data_ptr(), _stream(codes.device)), "lora_block8_decode")
+    return out
 
 
 def lora_device_status(reset: bool = True) -> int:

@@ -495,6 +495,10 @@ int launch_chain(const ChainParams& q, cudaStream_t stream);
 int launch_dense_patch(void* param, int param_dtype, const void* payload, int payload_dtype,
                        long long n, int kind, float k, cudaStream_t stream);
 
+// ------------------------------------------------------------------ norms
+// workspace bytes of lora_norm_bwd over [T, C]: a partial row of dw and db per CTA
+size_t norm_bwd_workspace(long long T, long long C);
+
 // ------------------------------------------------------------------ NF4 table (host)
 void nf4_codebook_host(float out[16]);
 
