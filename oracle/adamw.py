@@ -4,7 +4,9 @@ A block is 256 consecutive elements with one scale a (their largest magnitude). 
 for a sign(q) (|q| / 127)^2 (signed, first moments) or a (q / 255)^4 (unsigned, second moments).
 The codes are defined by the float32 sequence: divide by the scale, root (twice for the unsigned
 form), multiply by the largest code, round half to even, each step correctly rounded; an unsigned
-value above zero is never coded as zero.
+value above zero is never coded as zero.  A code's share u of the largest code is the rounded product of
+the code and the rounded reciprocal of the largest code; the value is u |u| a or (u u)(u u) a, each
+product rounded.
 """
 from __future__ import annotations
 
@@ -60,7 +62,7 @@ def encode(x, signed):
 def decode(q, top, signed):
     """float32 values of codes, by the float32 sequence."""
     b = _blocks(np.asarray(q).astype(f32))
-    u = (b / f32(127 if signed else 255)).astype(f32)
+    u = (b * (f32(1) / f32(127 if signed else 255))).astype(f32)
     u = (u * np.abs(u)).astype(f32) if signed else ((u * u).astype(f32) * (u * u).astype(f32)).astype(f32)
     with np.errstate(all="ignore"):
         return (u * top[:, None]).astype(f32).reshape(-1)[:np.asarray(q).size]

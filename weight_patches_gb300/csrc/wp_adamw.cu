@@ -155,15 +155,6 @@ __device__ __forceinline__ void store_codes(void* p, long long at, int n, bool v
     if (k < n) q[k] = static_cast<uint8_t>((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
 }
 
-// RN(q / d) for a whole number q <= 255 and d = 127 or 255: the rounded reciprocal's product
-// corrected once by its exact remainder (equal to the IEEE quotient for every q).
-template <int kD>
-__device__ __forceinline__ float code_share(float q) {
-  constexpr float y = 1.0f / kD;
-  const float t = __fmul_rn(q, y);
-  return __fmaf_rn(__fmaf_rn(-static_cast<float>(kD), t, q), y, t);
-}
-
 // the codes of one word (four elements) as values; a byte becomes a float through the low
 // mantissa bits of 2^23
 template <bool kSigned>
@@ -173,10 +164,10 @@ __device__ __forceinline__ void decode4(uint32_t w, float top, float* v) {
   for (int k = 0; k < 4; ++k) {
     const float f = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540 + k));
     if (kSigned) {
-      const float u = code_share<127>(__fsub_rn(f, 8388608.0f + 128.0f));
+      const float u = __fmul_rn(__fsub_rn(f, 8388608.0f + 128.0f), 1.0f / 127.0f);
       v[k] = __fmul_rn(__fmul_rn(u, fabsf(u)), top);
     } else {
-      const float u = code_share<255>(__fsub_rn(f, 8388608.0f));
+      const float u = __fmul_rn(__fsub_rn(f, 8388608.0f), 1.0f / 255.0f);
       const float u2 = __fmul_rn(u, u);
       v[k] = __fmul_rn(__fmul_rn(u2, u2), top);
     }
