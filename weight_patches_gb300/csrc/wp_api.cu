@@ -134,6 +134,16 @@ bool valid_output(const wp_out* y) {
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
+}  // namespace
+
+int encode_map_bf16(CUtensorMap* m, const void* ptr, long long inner, long long outer, long long ld, int box_inner,
+                    int box_outer, int swizzle) {
+  return make_map(m, WP_BF16, ptr, inner, outer, ld, box_inner, box_outer, swizzle);
+}
+unsigned long long device_wait_limit_ns() { return wait_limit_ns(); }
+
+namespace {
+
 struct FwdPlan {
   bool tc = false;        // tensor-core path
   int rank32_total = 0;   // fp32 adapters' total rank (tensor-core path)

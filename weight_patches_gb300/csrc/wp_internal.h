@@ -495,6 +495,34 @@ int launch_chain(const ChainParams& q, cudaStream_t stream);
 int launch_dense_patch(void* param, int param_dtype, const void* payload, int payload_dtype,
                        long long n, int kind, float k, cudaStream_t stream);
 
+// ------------------------------------------------------------------ adapters of many requests
+// What every kernel of lora_linear_fwd_multi knows of the call (wp_multi.cu).
+struct MultiCall {
+  int T, K, N, G, og;                    // og = N / G
+  int R, R16, S;                         // rank, a group's H~ columns (R rounded up to 16), slots
+  const uint16_t* X; long long ldx;
+  const uint16_t* A;                     // [S, G R, K]
+  const uint16_t* B;                     // [S, N, R]
+  const float* scale;
+  const int* slot;
+  const float* row_scale;
+  float request_scale;
+  uint16_t* H;                           // [T, G R16] bf16: s X A^T
+  int* act;                              // [T]: the row's slot, or -1 when it uses no adapter
+  const void* bias; int bias_f32;
+  void* Y; long long ldy; int y_f32;
+  int* status;
+  unsigned long long timeout_ns;
+};
+// Few rows (wp_multi_small.cu): H~ a (slot, 16 rank rows) per CTA, then W streamed once with the
+// rows as the MMA's width, K split over a cluster.
+int launch_multi_shrink_small(const MultiCall& c, cudaStream_t stream);
+int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStream_t stream);
+
+int encode_map_bf16(CUtensorMap* m, const void* ptr, long long inner, long long outer, long long ld, int box_inner,
+                    int box_outer, int swizzle);
+unsigned long long device_wait_limit_ns();
+
 // ------------------------------------------------------------------ norms
 // workspace bytes of lora_norm_bwd over [T, C]: a partial row of dw and db per CTA
 size_t norm_bwd_workspace(long long T, long long C);

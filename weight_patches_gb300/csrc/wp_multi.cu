@@ -19,24 +19,9 @@ namespace wp {
 
 namespace {
 
-struct MultiParams {
-  int T, K, N, G, R, R16, S;             // R16: a group's H~ columns (R rounded up to 16)
-  const uint16_t* X; long long ldx;
-  const uint16_t* A;                     // [S, G R, K]
-  const uint16_t* B;                     // [S, N, R]
-  const float* scale;
-  const int* slot;
-  const float* row_scale;
-  float request_scale;
-  uint16_t* H;                           // [T, G R16]
-  const float* base;                     // [T, N] or null
-  const void* bias; int bias_f32;        // when there is no base
-  void* Y; long long ldy; int y_f32;
-};
-
 __device__ __forceinline__ float bf2f(uint32_t h) { return __uint_as_float(h << 16); }
 
-__global__ void __launch_bounds__(256) multi_h_kernel(const MultiParams p) {
+__global__ void __launch_bounds__(256) multi_h_kernel(const MultiCall p) {
   const int t = blockIdx.x;
   const int a = p.slot[t];
   const int lane = threadIdx.x & 31;
@@ -65,13 +50,13 @@ __global__ void __launch_bounds__(256) multi_h_kernel(const MultiParams p) {
   }
 }
 
-__global__ void __launch_bounds__(256) multi_y_kernel(const MultiParams p) {
+__global__ void __launch_bounds__(256) multi_y_kernel(const MultiCall p, const float* base) {
   const int t = blockIdx.y;
   const int n = blockIdx.x * 256 + threadIdx.x;
   if (n >= p.N) return;
   const int a = p.slot[t];
   float y = 0.f;
-  if (p.base) y = p.base[static_cast<long long>(t) * p.N + n];
+  if (base) y = base[static_cast<long long>(t) * p.N + n];
   else if (p.bias) y = p.bias_f32 ? static_cast<const float*>(p.bias)[n] : bf2f(static_cast<const uint16_t*>(p.bias)[n]);
   if (a >= 0 && a < p.S) {
     const int g = n / (p.N / p.G);
@@ -118,6 +103,28 @@ int check(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
   return WP_OK;
 }
 
+// Rows up to which the weight-streaming kernels take a bf16 weight (or none).
+constexpr int kSmallRows = 512;
+bool small_rows(int T, const wp_mat* W) { return T <= kSmallRows && (!W || W->dtype == WP_BF16); }
+
+struct Layout {
+  size_t h = 0, act = 0, base = 0, fwd = 0, total = 0;
+};
+
+Layout layout(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
+  Layout L;
+  const size_t T = static_cast<size_t>(X->rows);
+  const size_t r16 = (bank->rank + 15) / 16 * 16;
+  L.act = r256(T * bank->n_groups * r16 * 2);
+  L.base = L.act + r256(T * 4);
+  L.total = L.fwd = L.base;
+  if (W && !small_rows(static_cast<int>(T), W)) {
+    L.fwd = L.base + r256(T * bank->out * 4);
+    L.total = L.fwd + r256(lora_workspace_size(WP_OP_FWD, X, W, nullptr, 0));
+  }
+  return L;
+}
+
 }  // namespace
 }  // namespace wp
 
@@ -127,11 +134,7 @@ extern "C" {
 
 size_t lora_multi_workspace_size(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
   if (check(X, W, bank) != WP_OK || X->rows == 0) return 0;
-  const size_t T = static_cast<size_t>(X->rows);
-  const size_t r16 = (bank->rank + 15) / 16 * 16;
-  size_t need = r256(T * bank->n_groups * r16 * 2);
-  if (W) need += r256(T * bank->out * 4) + r256(lora_workspace_size(WP_OP_FWD, X, W, nullptr, 0));
-  return need;
+  return layout(X, W, bank).total;
 }
 
 int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, const wp_bank* bank,
@@ -154,41 +157,55 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
   if (!al16(X->data) || X->ld % 8 || !al16(bank->A) || !al16(bank->B)) return WP_ERR_ALIGN;
   if (W && (!al16(W->data) || W->ld % 8)) return WP_ERR_ALIGN;
   if (!al16(Y->data) || Y->ld % (Y->dtype == WP_BF16 ? 8 : 4)) return WP_ERR_ALIGN;
-  const size_t need = lora_multi_workspace_size(X, W, bank);
-  if (!workspace || workspace_bytes < need) return WP_ERR_WORKSPACE;
+  const Layout L = layout(X, W, bank);
+  if (!workspace || workspace_bytes < L.total) return WP_ERR_WORKSPACE;
   if (!al16(workspace)) return WP_ERR_ALIGN;
 
-  MultiParams p{};
-  p.T = static_cast<int>(X->rows); p.K = static_cast<int>(X->cols); p.N = static_cast<int>(bank->out);
-  p.G = bank->n_groups; p.R = bank->rank; p.R16 = (p.R + 15) / 16 * 16; p.S = bank->n_slots;
-  p.X = static_cast<const uint16_t*>(X->data); p.ldx = X->ld;
-  p.A = static_cast<const uint16_t*>(bank->A); p.B = static_cast<const uint16_t*>(bank->B);
-  p.scale = bank->scale; p.slot = slot; p.row_scale = row_scale; p.request_scale = rs;
-  p.H = static_cast<uint16_t*>(workspace);
-  p.Y = Y->data; p.ldy = Y->ld; p.y_f32 = Y->dtype == WP_FP32;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (W) {
-    char* at = static_cast<char*>(workspace) + r256(static_cast<size_t>(p.T) * p.G * p.R16 * 2);
-    const wp_out base{at, WP_FP32, X->rows, bank->out, bank->out};
-    char* ws = at + r256(static_cast<size_t>(p.T) * p.N * 4);
-    rc = lora_linear_fwd(X, W, bias, nullptr, 0, 1.0, &base, ws, lora_workspace_size(WP_OP_FWD, X, W, nullptr, 0), stream);
-    if (rc != WP_OK) return rc;
-    p.base = reinterpret_cast<const float*>(at);
-  } else if (bias) {
-    p.bias = bias->data;
-    p.bias_f32 = bias->dtype == WP_FP32;
+  char* ws = static_cast<char*>(workspace);
+  MultiCall c{};
+  c.T = static_cast<int>(X->rows); c.K = static_cast<int>(X->cols); c.N = static_cast<int>(bank->out);
+  c.G = bank->n_groups; c.og = c.N / c.G;
+  c.R = bank->rank; c.R16 = (c.R + 15) / 16 * 16; c.S = bank->n_slots;
+  c.X = static_cast<const uint16_t*>(X->data); c.ldx = X->ld;
+  c.A = static_cast<const uint16_t*>(bank->A); c.B = static_cast<const uint16_t*>(bank->B);
+  c.scale = bank->scale; c.slot = slot; c.row_scale = row_scale; c.request_scale = rs;
+  c.H = reinterpret_cast<uint16_t*>(ws + L.h);
+  c.act = reinterpret_cast<int*>(ws + L.act);
+  if (bias) {
+    c.bias = bias->data;
+    c.bias_f32 = bias->dtype == WP_FP32;
   }
-  multi_h_kernel<<<p.T, 256, 0, st>>>(p);
-  for (int t0 = 0; t0 < p.T; t0 += 65535) {
-    MultiParams q = p;
-    const int nt = p.T - t0 < 65535 ? p.T - t0 : 65535;
-    q.T = nt;
+  c.Y = Y->data; c.ldy = Y->ld; c.y_f32 = Y->dtype == WP_FP32;
+  c.status = tc_status_ptr();
+  c.timeout_ns = device_wait_limit_ns();
+  if (!c.status) {
+    set_last_cuda_error(cudaGetLastError());
+    return WP_ERR_CUDA;
+  }
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (small_rows(c.T, W)) {
+    rc = launch_multi_shrink_small(c, st);
+    if (rc != WP_OK) return rc;
+    return launch_multi_small(c, W ? W->data : nullptr, W ? W->ld : 0, st);
+  }
+  const float* base = nullptr;
+  if (W) {
+    const wp_out by{ws + L.base, WP_FP32, X->rows, bank->out, bank->out};
+    rc = lora_linear_fwd(X, W, bias, nullptr, 0, 1.0, &by, ws + L.fwd, L.total - L.fwd, stream);
+    if (rc != WP_OK) return rc;
+    base = reinterpret_cast<const float*>(ws + L.base);
+    c.bias = nullptr;
+  }
+  multi_h_kernel<<<c.T, 256, 0, st>>>(c);
+  for (int t0 = 0; t0 < c.T; t0 += 65535) {
+    MultiCall q = c;
+    q.T = c.T - t0 < 65535 ? c.T - t0 : 65535;
     q.slot += t0;
     if (q.row_scale) q.row_scale += t0;
-    q.H += static_cast<long long>(t0) * p.G * p.R16;
-    if (q.base) q.base += static_cast<long long>(t0) * p.N;
-    q.Y = static_cast<char*>(p.Y) + static_cast<long long>(t0) * p.ldy * (p.y_f32 ? 4 : 2);
-    multi_y_kernel<<<dim3((p.N + 255) / 256, nt), 256, 0, st>>>(q);
+    q.H += static_cast<long long>(t0) * c.G * c.R16;
+    q.Y = static_cast<char*>(c.Y) + static_cast<long long>(t0) * c.ldy * (c.y_f32 ? 4 : 2);
+    multi_y_kernel<<<dim3((c.N + 255) / 256, q.T), 256, 0, st>>>(
+        q, base ? base + static_cast<long long>(t0) * c.N : nullptr);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

@@ -1,0 +1,486 @@
+// wp_multi_small.cu -- the many-adapter projection for a few rows (decode batches).
+//
+//   Y[t, g] = X[t] W_g^T + bias_g + s_t (X[t] A_{a,g}^T) B_{a,g}^T,   a = slot[t]
+//
+// With this few rows every byte of W, and of the A and B of each slot present, is read for a
+// handful of products, so HBM is the floor and the start-up of each kernel the next bound.  Two
+// kernels, the second started while the first runs (programmatic dependent launch):
+//
+//   shrink  one CTA per (slot present, 16 rank rows): its 8 warps take turns along K with loads
+//           straight from global into mma.sync fragments -- the rank rows are the 16-row operand,
+//           the slot's rows of X the 8-wide one, both through the same permutation of k so that
+//           every lane loads 16 consecutive bytes -- and leave H~ = bf16(s X A^T).  mma.sync
+//           rather than tcgen05: there is no tile to keep, a row belongs to one slot only.
+//   main    W^T tiles of 128 output columns as the M = 128 operand of tcgen05.mma and the rows of
+//           X (rounded up to 16) as its width, W and X by TMA.  K is split over a cluster of up to
+//           8 CTAs so that two CTAs per SM are streaming W from the first moment; while they do,
+//           eight more warps form the adapters' term of the CTA's share of the rows on the CUDA
+//           cores (B is read once per row and the products are few: 2 R per output), and the
+//           partial tiles meet through distributed shared memory, added in CTA order.
+#include <atomic>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "wp_internal.h"
+#include "wp_ptx.cuh"
+
+namespace wp {
+
+namespace {
+
+__device__ __forceinline__ float bf2f(uint32_t h) { return __uint_as_float(h << 16); }
+
+__device__ __forceinline__ uint4 ldg16(const uint16_t* p) {
+  return __ldg(reinterpret_cast<const uint4*>(p));
+}
+
+// D[16 x 8] += A[16 x 16] B[16 x 8], bf16 inputs, fp32 sums
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+constexpr int kShrinkThreads = 256;
+constexpr int kShrinkWarps = kShrinkThreads / 32;
+constexpr int kMaxSmallT = 1024;          // rows a call of these kernels may have
+
+// H~ of up to 8 NT rows (list[0 .. n)) for 16 rank rows, K split over the warps; the partial
+// sums go to red[warp][16][8 NT].  U: 32-wide k steps whose loads are issued together.
+template <int NT, int U>
+__device__ __forceinline__ void shrink_pass(const MultiCall& c, const uint16_t* a_row0, const uint16_t* a_row1,
+                                            const int* list, int n, float* red) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kl = (lane & 3) * 8;                   // this lane's 8 k of every 32
+  const uint16_t* x[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int j = i * 8 + (lane >> 2);
+    x[i] = c.X + static_cast<long long>(list[j < n ? j : 0]) * c.ldx;
+  }
+  float d[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d[i][k] = 0.f;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int k0 = warp * (32 * U); k0 < c.K; k0 += kShrinkWarps * 32 * U) {
+    uint4 a0[U], a1[U], b[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * 32 + kl;
+      const bool ok = k < c.K;
+      a0[u] = ok ? ldg16(a_row0 + k) : zero;
+      a1[u] = ok ? ldg16(a_row1 + k) : zero;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) b[u][i] = ok ? ldg16(x[i] + k) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        mma_16816(d[i], a0[u].x, a1[u].x, a0[u].y, a1[u].y, b[u][i].x, b[u][i].y);
+        mma_16816(d[i], a0[u].z, a1[u].z, a0[u].w, a1[u].w, b[u][i].z, b[u][i].w);
+      }
+  }
+  // d[i][0..1]: rank row lane / 4, X rows 8 i + 2 (lane % 4) + {0, 1}; d[i][2..3]: rank row + 8
+  float* out = red + warp * (16 * 8 * NT);
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int col = i * 8 + (lane & 3) * 2;
+    float* o = out + (lane >> 2) * (8 * NT) + col;
+    o[0] = d[i][0];
+    o[1] = d[i][1];
+    o[8 * 8 * NT] = d[i][2];
+    o[8 * 8 * NT + 1] = d[i][3];
+  }
+}
+
+__global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(const MultiCall c) {
+  __shared__ int list[kMaxSmallT];
+  __shared__ int wcount[kShrinkWarps];
+  __shared__ float red[kShrinkWarps * 16 * 32];
+  const int t = blockIdx.x, chunk = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_launch_dependents();
+  const int a = c.slot[t];
+  if (a < 0 || a >= c.S) {
+    if (chunk == 0 && tid == 0) c.act[t] = -1;
+    return;
+  }
+  // the rows of this slot, in order; the first of them stands for the slot
+  int n = 0;
+  bool earlier = false;
+  for (int base = 0; base < c.T; base += kShrinkThreads) {
+    const int j = base + tid;
+    const bool mine = j < c.T && c.slot[j] == a;
+    earlier = earlier || (mine && j < t);
+    const uint32_t m = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) wcount[warp] = __popc(m);
+    if (__syncthreads_or(earlier)) return;
+    int at = n;
+    for (int w = 0; w < kShrinkWarps; ++w) {
+      if (w < warp) at += wcount[w];
+      n += wcount[w];
+    }
+    if (mine) list[at + __popc(m & ((1u << lane) - 1))] = j;
+    __syncthreads();
+  }
+  const int rows = c.G * c.R;
+  const int j0 = chunk * 16;
+  const uint16_t* A = c.A + static_cast<long long>(a) * rows * c.K;
+  // rank rows past the last repeat it; their sums are not kept
+  const uint16_t* a_row0 = A + static_cast<long long>(min(j0 + (lane >> 2), rows - 1)) * c.K;
+  const uint16_t* a_row1 = A + static_cast<long long>(min(j0 + 8 + (lane >> 2), rows - 1)) * c.K;
+  const float sa = c.scale[a];
+  for (int p0 = 0; p0 < n;) {
+    const int left = n - p0;
+    const int nt = left <= 8 ? 1 : 4;
+    const int np = left < 8 * nt ? left : 8 * nt;
+    if (nt == 1) shrink_pass<1, 4>(c, a_row0, a_row1, list + p0, np, red);
+    else shrink_pass<4, 2>(c, a_row0, a_row1, list + p0, np, red);
+    __syncthreads();
+    for (int i = tid; i < 16 * np; i += kShrinkThreads) {
+      const int r = i / np, col = i - r * np;          // rank row of the chunk, row of the pass
+      const int j = j0 + r;
+      if (j >= rows) continue;
+      float h = 0.f;
+#pragma unroll
+      for (int w = 0; w < kShrinkWarps; ++w) h += red[(w * 16 + r) * (8 * nt) + col];
+      const int tt = list[p0 + col];
+      float s = sa;
+      if (c.row_scale) s = __fmul_rn(s, c.row_scale[tt]);
+      s = __fmul_rn(s, c.request_scale);
+      const int g = j / c.R, rr = j - g * c.R;
+      uint16_t* out = c.H + static_cast<long long>(tt) * c.G * c.R16 + g * c.R16 + rr;
+      uint16_t hb;
+      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(hb) : "f"(h * s));
+      *out = hb;
+      if (c.R != c.R16 && rr >= c.R - 8) out[8] = 0;   // the group's padding columns
+      if (j == 0) c.act[tt] = s != 0.f ? a : -1;
+    }
+    __syncthreads();
+    p0 += np;
+  }
+}
+
+// ------------------------------------------------------------------------------ main
+struct SmallMaps {
+  CUtensorMap x, w;            // boxes of 64 K x t16 rows / 128 rows, 128-byte swizzle
+};
+
+constexpr int kSmallThreads = 384;         // warp 0 TMA, warp 1 MMA, warps 4..11 the adapters' term and the output
+constexpr int kSmallSmem = 113 * 1024 - 1024;   // two CTAs per SM
+constexpr int kSmallMaxStages = 8;
+
+struct SmallParams {
+  MultiCall c;
+  int has_w;
+  int tile;                    // rows of X per tile (128, or 64 where shared memory holds no more)
+  int t16;                     // MMA width: rows of a tile rounded up to 16
+  int splits, kb_per, k_blocks;
+  int share;                   // rows of the tile whose output a CTA of the cluster writes
+  int stages, stage_bytes;
+  uint32_t tmem_cols;
+};
+
+__global__ void __launch_bounds__(kSmallThreads, 2)
+    multi_small_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant__ SmallParams p) {
+  const MultiCall& c = p.c;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base_addr = (raw_addr + 1023u) & ~1023u;
+  uint8_t* sbase = smem_raw + (base_addr - raw_addr);
+  float* part = reinterpret_cast<float*>(sbase);                       // [t16][128], over the drained stages
+  float* delta = reinterpret_cast<float*>(sbase + p.stages * p.stage_bytes);   // [share][128]
+  int* act = reinterpret_cast<int*>(delta + p.share * 128);            // [share]
+  __shared__ uint64_t full[kSmallMaxStages], empty[kSmallMaxStages], acc_full;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.stages;
+  const int rank = p.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int n0 = static_cast<int>(blockIdx.x) / p.splits * 128;
+  const int t0 = static_cast<int>(blockIdx.y) * p.tile;
+  const int nt = min(p.tile, c.T - t0);
+  const int kb0 = rank * p.kb_per, kb1 = min(p.k_blocks, kb0 + p.kb_per);
+  const int r0 = rank * p.share, cnt = max(0, min(nt - r0, p.share));  // this CTA's rows of the tile
+  const uint64_t tmo = c.timeout_ns;
+  int* status = c.status;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&acc_full, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0 && p.has_w) {
+      const uint64_t keep = l2_evict_last(), once = gridDim.y > 1 ? keep : l2_evict_first();
+      uint32_t issued = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+        const uint32_t s = issued % S;
+        if (issued >= static_cast<uint32_t>(S) &&
+            !(ok = mbar_wait(&empty[s], ((issued / S) & 1u) ^ 1u, abort_flag, tmo, status)))
+          break;
+        uint8_t* st = sbase + s * p.stage_bytes;
+        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(p.stage_bytes));
+        tma_load_2d_hint(st, &maps.w, kb * kBK, n0, &full[s], once);
+        tma_load_2d_hint(st + kATileBytes, &maps.x, kb * kBK, t0, &full[s], keep);
+      }
+      if (!ok)                                        // copies in flight land before the CTA leaves
+        for (uint32_t s = 0; s < static_cast<uint32_t>(S); ++s) {
+          const uint32_t uses = issued / S + (s < issued % S ? 1u : 0u);
+          if (uses == 0) continue;
+          const uint64_t b = globaltimer_ns();
+          while (!mbar_try_wait(smem_u32(&full[s]), (uses - 1) & 1u) && globaltimer_ns() - b < 100000000ull) {
+          }
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && p.has_w) {
+      const uint32_t idesc = idesc_bf16_f32(128, static_cast<uint32_t>(p.t16));
+      const uint32_t u_w = smem_u32(sbase) >> 4;
+      uint32_t step = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, ++step) {
+        const uint32_t s = step % S;
+        if (!(ok = mbar_wait(&full[s], (step / S) & 1u, abort_flag, tmo, status))) break;
+        tc_fence_after();
+        const uint32_t at = u_w + s * (static_cast<uint32_t>(p.stage_bytes) >> 4);
+        const uint64_t ad = kDescSw128K | at, bd = kDescSw128K | (at + (kATileBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk)
+          mma_bf16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (step > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&empty[s]);
+      }
+      mma_commit(&acc_full);
+      if (!ok) {                                      // the MMAs issued finish before tensor memory is freed
+        const uint64_t b = globaltimer_ns();
+        while (!mbar_try_wait(smem_u32(&acc_full), 0) && globaltimer_ns() - b < 100000000ull) {
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------ the adapters' term of this CTA's rows
+    const int row = (warp & 3) * 32 + lane;           // output column n0 + row = TMEM lane
+    const int half = (warp - 4) >> 2;
+    const int n = n0 + row;
+    const bool n_ok = n < c.N;
+    const int tid = threadIdx.x - 128;
+    grid_dependency_wait();                           // H~ and act
+    for (int i = tid; i < cnt; i += 256) act[i] = c.act[t0 + r0 + i];
+    named_bar_sync(1, 256);
+    const int g = n_ok ? n / c.og : 0;
+    const uint16_t* Hg = c.H + static_cast<long long>(t0 + r0) * c.G * c.R16 + g * c.R16;
+    const int hld = c.G * c.R16;
+    constexpr int U = 4;
+    for (int i0 = half; i0 < cnt; i0 += 2 * U) {
+      const uint16_t* b[U];
+      const uint16_t* h[U];
+      float acc[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + 2 * u;
+        const int a = i < cnt && n_ok ? act[i] : -1;
+        acc[u] = 0.f;
+        b[u] = a >= 0 ? c.B + (static_cast<long long>(a) * c.N + n) * c.R : nullptr;
+        h[u] = Hg + static_cast<long long>(i < cnt ? i : 0) * hld;
+      }
+#pragma unroll 2
+      for (int r = 0; r < c.R; r += 8) {
+        uint4 bv[U], hv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (b[u]) {
+            bv[u] = ldg16(b[u] + r);
+            hv[u] = *reinterpret_cast<const uint4*>(h[u] + r);
+          } else {
+            bv[u] = hv[u] = make_uint4(0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t bw[4] = {bv[u].x, bv[u].y, bv[u].z, bv[u].w};
+          const uint32_t hw[4] = {hv[u].x, hv[u].y, hv[u].z, hv[u].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            acc[u] = fmaf(bf2f(hw[k] & 0xffffu), bf2f(bw[k] & 0xffffu), acc[u]);
+            acc[u] = fmaf(__uint_as_float(hw[k] & 0xffff0000u), __uint_as_float(bw[k] & 0xffff0000u), acc[u]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + 2 * u < cnt) delta[(i0 + 2 * u) * 128 + row] = acc[u];
+    }
+    // ------------------------------------------------ the accumulator into shared memory
+    if (p.has_w) {
+      const bool ok = mbar_wait(&acc_full, 0, abort_flag, tmo, status);
+      if (__all_sync(0xffffffffu, ok) && kb1 > kb0) {
+        tc_fence_after();
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        for (int col = half * 8; col < p.t16; col += 16) {
+          uint32_t r8[8];
+          tmem_ld8(tmem + lane_base + col, r8);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) part[(col + i) * 128 + row] = __uint_as_float(r8[i]);
+        }
+        tc_fence_before();
+      } else {
+        for (int col = half; col < p.t16; col += 2) part[col * 128 + row] = 0.f;
+      }
+    }
+  }
+  __syncthreads();
+  if (p.splits > 1) cluster_sync();                   // every CTA's partial tile is in place
+  if (warp >= 4) {
+    // one row of X per warp, 4 output columns per lane: the splits' sums in CTA order
+    const int n = n0 + lane * 4;
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if (c.bias && n < c.N) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        bias[k] = c.bias_f32 ? static_cast<const float*>(c.bias)[n + k] : bf2f(static_cast<const uint16_t*>(c.bias)[n + k]);
+    }
+    for (int i = warp - 4; i < cnt; i += 8) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (p.has_w) {
+        const uint32_t at = smem_u32(part + (r0 + i) * 128 + lane * 4);
+        if (p.splits > 1) {
+          float4 q[8];
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            const uint32_t ra = mapa_shared(at, static_cast<uint32_t>(min(s, p.splits - 1)));
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(q[s].x), "=f"(q[s].y), "=f"(q[s].z), "=f"(q[s].w)
+                         : "r"(ra));
+          }
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            if (s < p.splits) {
+              v[0] += q[s].x; v[1] += q[s].y; v[2] += q[s].z; v[3] += q[s].w;
+            }
+        } else {
+          const float4 q = *reinterpret_cast<const float4*>(part + (r0 + i) * 128 + lane * 4);
+          v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        }
+      }
+      const float4 d = *reinterpret_cast<const float4*>(delta + i * 128 + lane * 4);
+      v[0] = (v[0] + bias[0]) + d.x;
+      v[1] = (v[1] + bias[1]) + d.y;
+      v[2] = (v[2] + bias[2]) + d.z;
+      v[3] = (v[3] + bias[3]) + d.w;
+      if (n < c.N) {
+        const long long o = static_cast<long long>(t0 + r0 + i) * c.ldy + n;
+        if (c.y_f32) *reinterpret_cast<float4*>(static_cast<float*>(c.Y) + o) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.Y) + o) =
+              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (p.splits > 1) cluster_sync();                   // no CTA leaves while a peer reads its tile
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+int fail(cudaError_t e) {
+  set_last_cuda_error(e);
+  return WP_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_multi_shrink_small(const MultiCall& c, cudaStream_t stream) {
+  multi_shrink_small_kernel<<<dim3(c.T, (c.G * c.R + 15) / 16), kShrinkThreads, 0, stream>>>(c);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? WP_OK : fail(e);
+}
+
+int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};              // devices whose shared-memory limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(e);
+  if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1u)) {
+    e = cudaFuncSetAttribute(multi_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+    if (e != cudaSuccess) return fail(e);
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  SmallParams p{};
+  p.c = c;
+  p.has_w = W ? 1 : 0;
+  p.k_blocks = (c.K + kBK - 1) / kBK;
+  const int n_tiles = (c.N + 127) / 128;
+  int t_tiles = 0;
+  size_t smem = 0;
+  for (p.tile = 128;; p.tile /= 2) {
+    if (p.tile < 64) return WP_ERR_UNSUPPORTED;
+    const int tile = c.T < p.tile ? c.T : p.tile;
+    t_tiles = (c.T + p.tile - 1) / p.tile;
+    p.t16 = (tile + 15) / 16 * 16;
+    p.tmem_cols = p.t16 <= 32 ? 32 : (p.t16 <= 64 ? 64 : 128);
+    // K splits: the most (a power of two up to 8) that two CTAs per SM hold at once, each with at
+    // least two K blocks
+    p.splits = 1;
+    while (p.splits < 8 && 2ll * p.splits * n_tiles * t_tiles <= 2ll * device_sm_count() && p.k_blocks >= 4 * p.splits)
+      p.splits *= 2;
+    p.kb_per = (p.k_blocks + p.splits - 1) / p.splits;
+    p.share = (tile + p.splits - 1) / p.splits;
+    p.stage_bytes = kATileBytes + p.t16 * 128;
+    const int delta_bytes = p.share * (128 + 1) * 4 + 16;
+    p.stages = (kSmallSmem - 1024 - delta_bytes) / p.stage_bytes;
+    if (p.stages > kSmallMaxStages) p.stages = kSmallMaxStages;
+    if (p.stages > p.kb_per) p.stages = p.kb_per;
+    // the partial tile [t16][128] fp32 lies over the stages
+    while (p.stages * p.stage_bytes < p.t16 * 512) ++p.stages;
+    smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + delta_bytes;
+    if (smem <= static_cast<size_t>(kSmallSmem) && p.stages <= kSmallMaxStages) break;
+  }
+  SmallMaps maps{};
+  int rc = encode_map_bf16(&maps.x, c.X, c.K, c.T, c.ldx, kBK, p.t16, 128);
+  if (rc == WP_OK && W) rc = encode_map_bf16(&maps.w, W, c.K, c.N, ldw, kBK, 128, 128);
+  if (rc != WP_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_tiles * p.splits, t_tiles);
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, multi_small_kernel, maps, p);
+  return e == cudaSuccess ? WP_OK : fail(e);
+}
+
+}  // namespace wp
