@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -110,16 +111,17 @@ def _load():
     lib.lora_swiglu_bwd.argtypes = [pm, pm, po, po, P]
     lib.lora_dense_patch.argtypes = [P, I32, I64, P, I32, I64, I32, D, P]
     pb = ctypes.POINTER(WpBank)
-    pt, pp, pg = ctypes.POINTER(WpAdamWTensor), ctypes.POINTER(WpAdamWPlan), ctypes.POINTER(WpAdamWArgs)
-    lib.lora_linear_fwd_multi.argtypes = [pm, pm, pm, pb, P, P, D, po, P, SZ, P]
+    pt, pp = ctypes.POINTER(WpAdamWTensor), ctypes.POINTER(WpAdamWPlan)
+    # the calls of decode and training steps take their structs as packed bytes (_pmat, _pout)
+    lib.lora_linear_fwd_multi.argtypes = [P, P, P, P, P, P, D, P, P, SZ, P]
     lib.lora_multi_workspace_size.argtypes = [pm, pm, pb]
     lib.lora_multi_workspace_size.restype = SZ
-    lib.lora_norm_fwd.argtypes = [pm, pm, pm, I32, D, po, P, P]
-    lib.lora_norm_bwd.argtypes = [pm, pm, pm, P, I32, po, po, po, P, SZ, P]
+    lib.lora_norm_fwd.argtypes = [P, P, P, I32, D, P, P, P]
+    lib.lora_norm_bwd.argtypes = [P, P, P, P, I32, P, P, P, P, SZ, P]
     lib.lora_adamw_plan_size.argtypes = [pt, I32]
     lib.lora_adamw_plan_size.restype = SZ
     lib.lora_adamw_plan_init.argtypes = [pt, I32, P, SZ, pp, P]
-    lib.lora_adamw_step.argtypes = [pp, ctypes.POINTER(P), I32, pg, P]
+    lib.lora_adamw_step.argtypes = [P, P, I32, P, P]
     lib.lora_block8_decode.argtypes = [P, I32, P, I64, P, P]
     lib.lora_workspace_size.argtypes = [I32, pm, pm, pa, I32]
     lib.lora_workspace_size.restype = SZ
@@ -213,6 +215,34 @@ def _ref(m):
 
 def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+# Marshalling of the calls whose kernels take microseconds: a struct as packed bytes costs a tenth
+# of a ctypes.Structure, the raw stream handle a twentieth of a Stream object.
+_pack_mat = struct.Struct("@PiqqqP").pack        # wp_mat
+_pack_adamw = struct.Struct("@ddddddqP").pack    # wp_adamw_args
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _pmat(t) -> Optional[bytes]:
+    if t is None:
+        return None
+    if isinstance(t, NF4Weight):
+        return bytes(_mat(t))
+    shape = t.shape
+    if len(shape) == 2:
+        ld, one = t.stride()
+        if one != 1 and shape[1] != 1:
+            raise ValueError("expected a 2-D row-major tensor (stride(1) == 1)")
+        return _pack_mat(t.data_ptr(), _DT[t.dtype], shape[0], shape[1], ld if shape[0] > 1 else max(ld, shape[1]), 0)
+    if len(shape) != 1 or not t.is_contiguous():
+        raise ValueError("expected a row-major matrix or a contiguous vector")
+    return _pack_mat(t.data_ptr(), _DT[t.dtype], 1, shape[0], shape[0], 0)
+
+
+def _pout(t: torch.Tensor) -> bytes:
+    return _pmat(t)[:40]                          # wp_out: wp_mat without its last pointer
 
 
 def _check(status: int, where: str):
@@ -439,12 +469,10 @@ class AdapterBank:
         if not A.device == B.device == scale.device:
             raise ValueError("AdapterBank tensors must be on one device")
         self.A, self.B, self.scale, self.n_groups = A, B, scale, n_groups
+        self.out_features = B.shape[1]
         self._c = WpBank(A.data_ptr(), B.data_ptr(), scale.data_ptr(), _DT[A.dtype], A.shape[0], n_groups,
                          B.shape[2], A.shape[2], B.shape[1])
-
-    @property
-    def out_features(self) -> int:
-        return self.B.shape[1]
+        self._packed = bytes(self._c)
 
 
 def lora_multi_workspace_size(X: torch.Tensor, W, bank: AdapterBank) -> int:
@@ -459,23 +487,22 @@ def lora_linear_fwd_multi(X: torch.Tensor, W, bias: Optional[torch.Tensor], bank
     bank, -1 by convention, uses no adapter) and s_t = bank.scale[a] * row_scale[t] * request_scale;
     with ``bank.n_groups`` > 1, per stacked column group.  W bf16, ``NF4Weight`` or None."""
     T = X.shape[0]
-    if slot.dtype != torch.int32 or slot.numel() != T or not slot.is_contiguous():
+    if slot.dtype is not torch.int32 or slot.numel() != T or not slot.is_contiguous():
         raise ValueError("slot must be a contiguous int32 tensor with one entry per row of X")
-    if row_scale is not None and (row_scale.dtype != torch.float32 or row_scale.numel() != T
+    if row_scale is not None and (row_scale.dtype is not torch.float32 or row_scale.numel() != T
                                   or not row_scale.is_contiguous()):
         raise ValueError("row_scale must be a contiguous float32 tensor with one entry per row of X")
     if out is None:
-        out = torch.empty(T, bank._c.out, dtype=out_dtype, device=X.device)
-    lib, bank_c = _load(), ctypes.byref(bank._c)
-    xm, wm, bm, ym = _mat(X), _ref(_mat(W)), _ref(_mat(bias)), _out(out)
+        out = torch.empty(T, bank.out_features, dtype=out_dtype, device=X.device)
+    lib = _load()
     if workspace is None:
-        need = lib.lora_multi_workspace_size(ctypes.byref(xm), wm, bank_c)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
-    st = lib.lora_linear_fwd_multi(ctypes.byref(xm), wm, bm, bank_c, slot.data_ptr(),
-                                   None if row_scale is None else row_scale.data_ptr(), request_scale,
-                                   ctypes.byref(ym), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream(X.device))
-    _check(st, "lora_linear_fwd_multi")
+        workspace = torch.empty(max(lora_multi_workspace_size(X, W, bank), 1), dtype=torch.uint8, device=X.device)
+    st = lib.lora_linear_fwd_multi(_pmat(X), _pmat(W), _pmat(bias), bank._packed, slot.data_ptr(),
+                                   None if row_scale is None else row_scale.data_ptr(), request_scale, _pout(out),
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   _raw_stream(X.get_device()))
+    if st:
+        _check(st, "lora_linear_fwd_multi")
     return out
 
 
@@ -489,10 +516,12 @@ def lora_norm_fwd(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
         out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
     if stats is None:
         stats = torch.empty(2, X.shape[0], dtype=torch.float32, device=X.device)
-    _check_stats(stats, X.shape[0])
-    st = _load().lora_norm_fwd(ctypes.byref(_mat(X)), _ref(_vec(weight)), _ref(_vec(bias)), kind, eps,
-                               ctypes.byref(_out(out)), stats.data_ptr(), _stream(X.device))
-    _check(st, "lora_norm_fwd")
+    else:
+        _check_stats(stats, X.shape[0])
+    st = _load().lora_norm_fwd(_pmat(X), _pvec(weight), _pvec(bias), kind, eps, _pout(out), stats.data_ptr(),
+                               _raw_stream(X.get_device()))
+    if st:
+        _check(st, "lora_norm_fwd")
     return out, stats
 
 
@@ -504,29 +533,28 @@ def lora_norm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: Optional[torch.Tens
                   kind: int = WP_NORM_LAYER, need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
                   workspace: Optional[torch.Tensor] = None):
     """(dX, dW, dB) of ``lora_norm_fwd`` from its stats; dW and dB fp32 [C], None where not asked for."""
-    _check_stats(stats, X.shape[0])
     T, C = X.shape
-    dx = torch.empty(T, C, dtype=X.dtype, device=X.device) if need_dx else None
-    dw = torch.empty(C, dtype=torch.float32, device=X.device) if need_dw else None
-    db = torch.empty(C, dtype=torch.float32, device=X.device) if need_db else None
-    xm = _mat(X)
-    vec = lambda t: None if t is None else ctypes.byref(WpOut(t.data_ptr(), WP_FP32, 1, C, C))  # noqa: E731
+    _check_stats(stats, T)
+    dev = X.device
+    dx = torch.empty(T, C, dtype=X.dtype, device=dev) if need_dx else None
+    dw = torch.empty(C, dtype=torch.float32, device=dev) if need_dw else None
+    db = torch.empty(C, dtype=torch.float32, device=dev) if need_db else None
     if workspace is None and (need_dw or need_db):
-        need = _load().lora_workspace_size(WP_OP_NORM_BWD, ctypes.byref(xm), None, None, 0)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
-    st = _load().lora_norm_bwd(ctypes.byref(_mat(dY)), ctypes.byref(xm), _ref(_vec(weight)), stats.data_ptr(), kind,
-                               None if dx is None else ctypes.byref(_out(dx)), vec(dw), vec(db),
-                               None if workspace is None else workspace.data_ptr(),
+        workspace = torch.empty(max(lora_norm_bwd_workspace_size(X), 1), dtype=torch.uint8, device=dev)
+    st = _load().lora_norm_bwd(_pmat(dY), _pmat(X), _pvec(weight), stats.data_ptr(), kind,
+                               None if dx is None else _pout(dx), None if dw is None else _pout(dw),
+                               None if db is None else _pout(db), None if workspace is None else workspace.data_ptr(),
                                0 if workspace is None else workspace.numel() * workspace.element_size(),
-                               _stream(X.device))
-    _check(st, "lora_norm_bwd")
+                               _raw_stream(X.get_device()))
+    if st:
+        _check(st, "lora_norm_bwd")
     return dx, dw, db
 
 
-def _vec(t: Optional[torch.Tensor]) -> Optional[WpMat]:
-    if t is not None and (t.dim() != 1 or not t.is_contiguous()):
+def _pvec(t: Optional[torch.Tensor]) -> Optional[bytes]:
+    if t is not None and t.dim() != 1:
         raise ValueError("weight and bias of a norm must be contiguous vectors")
-    return _mat(t)
+    return _pmat(t)
 
 
 def _check_stats(stats: torch.Tensor, T: int):
@@ -553,8 +581,9 @@ class AdamWPlan:
     """A prepared set of tensors (``lora_adamw_plan``); keeps the tensors and the device table."""
 
     def __init__(self, c: WpAdamWPlan, table: torch.Tensor, tensors, numels):
-        self._c, self._table, self._tensors, self._numels = c, table, tensors, numels
-        self._ptrs = (ctypes.c_void_p * len(numels))()
+        self._table, self._tensors, self._numels = table, tensors, numels
+        self._packed = bytes(c)
+        self._pack_ptrs = struct.Struct(f"@{len(numels)}P").pack
 
 
 def lora_adamw_plan(params: Sequence[torch.Tensor], m: Sequence, v: Sequence,
@@ -603,26 +632,24 @@ def lora_adamw_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor]], lr
     that multiplies the gradients as well (a clip or loss scale)."""
     if len(grads) != len(plan._numels):
         raise ValueError("lora_adamw_step: one gradient (or None) per tensor")
-    dtype, ptrs = None, plan._ptrs
-    for i, (g, numel) in enumerate(zip(grads, plan._numels)):
-        if g is None:
-            ptrs[i] = None
-            continue
-        if dtype is None:
-            dtype = g.dtype
-        if g.dtype != dtype or g.numel() != numel or not g.is_contiguous():
-            raise ValueError(f"lora_adamw_step: gradient {i} has another dtype, size or layout")
-        ptrs[i] = g.data_ptr()
-    if dtype is None:
+    given = [g for g in grads if g is not None]
+    if not given:
         return
+    dtype = given[0].dtype
     if dtype not in _DT:
         raise ValueError("lora_adamw_step: gradients must be fp32 or bf16")
+    numels = plan._numels if len(given) == len(grads) else [n for g, n in zip(grads, plan._numels) if g is not None]
+    if [g.numel() for g in given] != numels or {g.dtype for g in given} != {dtype} \
+            or not all([g.is_contiguous() for g in given]):
+        raise ValueError("lora_adamw_step: a gradient has another dtype, size or layout than its tensor's")
     if grad_scale_tensor is not None and (grad_scale_tensor.dtype != torch.float32 or grad_scale_tensor.numel() != 1):
         raise ValueError("grad_scale_tensor must be one float32 value")
-    args = WpAdamWArgs(lr, beta1, beta2, eps, weight_decay, grad_scale, step,
-                       None if grad_scale_tensor is None else grad_scale_tensor.data_ptr())
-    _check(_load().lora_adamw_step(ctypes.byref(plan._c), ptrs, _DT[dtype], ctypes.byref(args),
-                                   _stream(plan._table.device)), "lora_adamw_step")
+    ptrs = plan._pack_ptrs(*[0 if g is None else g.data_ptr() for g in grads])
+    args = _pack_adamw(lr, beta1, beta2, eps, weight_decay, grad_scale, step,
+                       0 if grad_scale_tensor is None else grad_scale_tensor.data_ptr())
+    st = _load().lora_adamw_step(plan._packed, ptrs, _DT[dtype], args, _raw_stream(plan._table.get_device()))
+    if st:
+        _check(st, "lora_adamw_step")
 
 
 def lora_block8_decode(codes: torch.Tensor, absmax: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -635,7 +662,7 @@ def lora_block8_decode(codes: torch.Tensor, absmax: torch.Tensor, out: Optional[
     elif out.dtype != torch.float32 or out.numel() != codes.numel() or not out.is_contiguous():
         raise ValueError("lora_block8_decode: out must be contiguous fp32 of the codes' size")
     _check(_load().lora_block8_decode(codes.data_ptr(), codes.dtype == torch.int8, absmax.data_ptr(), codes.numel(),
-                                      out.data_ptr(), _stream(codes.device)), "lora_block8_decode")
+                                      out.data_ptr(), _raw_stream(codes.get_device())), "lora_block8_decode")
     return out
 
 
