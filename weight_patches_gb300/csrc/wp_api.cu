@@ -909,6 +909,67 @@ int fwd_impl(const wp_mat* X, const wp_mat* W, const wp_mat* bias, int G, bool g
   return launch_tc_fwd(maps, p, 2 * pairs, smem, stream, nf4);
 }
 
+}  // namespace
+
+// The fused forward over rows of many adapters: the blocks' entries and H~ are already written (or
+// being written by the kernel launched just before).  Arguments are validated by the caller.
+int multi_fused(const MultiCall& c, const wp_mat* W, cudaStream_t stream) {
+  const bool nf4 = W && W->dtype == WP_NF4;
+  TcParams p{};
+  TcMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  p.T = c.T; p.K = c.K; p.N = c.N;
+  p.out_g = c.og; p.G = c.G;
+  p.nt_g = (c.og + kBN - 1) / kBN;
+  p.m_shift = nf4 ? 1 : 0;
+  p.r_blocks = (c.T + kPairM - 1) / kPairM;
+  p.m_tiles = (c.T + (kPairM << p.m_shift) - 1) / (kPairM << p.m_shift);
+  const long long total = static_cast<long long>(p.m_tiles) * c.G * p.nt_g;
+  if (total > 0x7FFFFFFFLL) return WP_ERR_UNSUPPORTED;
+  p.total_tiles = static_cast<int>(total);
+  p.k_blocks = (c.K + kBK - 1) / kBK;
+  p.has_base = W ? 1 : 0;
+  p.bias = c.bias; p.bias_f32 = c.bias_f32;
+  p.bias_vec = c.bias && aligned16(c.bias) ? 1 : 0;
+  p.Y = c.Y; p.ldy = c.ldy; p.y_f32 = c.y_f32;
+  p.ent = c.ent; p.ent_n = c.ent_n; p.ent_rows = c.ent_rows; p.ent_ld = c.ent_ld;
+  p.m_r16 = c.R16;
+  p.m_chunks = (c.R16 + 63) / 64;
+  p.timeout_ns = wait_limit_ns();
+  p.stage_bytes = nf4 ? kMHalvesNF4 * kATileBytes + kBHalfBytes : kATileBytes + kBHalfBytes;
+  const size_t fixed = 1024 + 2 * kStgBytes + 512;
+  p.stages = nf4 ? 3 : std::min<int>(kMaxStages, static_cast<int>((kSmemLimit - fixed) / p.stage_bytes));
+  if (nf4)
+    p.code_slots = std::min<int>(
+        kMaxCodeSlots, static_cast<int>((kSmemLimit - fixed - static_cast<size_t>(p.stages) * p.stage_bytes) / kCodeSlotBytes));
+  const size_t smem = fixed + static_cast<size_t>(p.stages) * p.stage_bytes + static_cast<size_t>(p.code_slots) * kCodeSlotBytes;
+  int rc = make_map_bf16(&maps.x, c.X, c.K, c.T, c.ldx, kBK, kBM);
+  if (rc == WP_OK && nf4) {
+    rc = make_map_u8(&maps.wq, W->data, c.K / 2, c.N, c.K / 2, kBK / 2, 128, 32);
+    p.absmax = W->absmax;
+    p.am_tma = (c.K % 256 == 0 && aligned16(W->absmax)) ? 1 : 0;
+    if (rc == WP_OK && p.am_tma) rc = make_map(&maps.am, WP_FP32, W->absmax, c.K / 64, c.N, c.K / 64, 4, 128, /*swizzle=*/0);
+    nf4_codebook_host(p.nf4_code);
+  } else if (rc == WP_OK && W) {
+    rc = make_map_bf16(&maps.w, W->data, c.K, c.N, W->ld, kBK, 128);
+  }
+  if (rc == WP_OK)
+    rc = make_map(&maps.y, c.y_f32 ? WP_FP32 : WP_BF16, c.Y, c.N, c.T, c.ldy, c.y_f32 ? 32 : 64, kBM);
+  // H~ and the bank's B in chunks of 64 ranks (128-byte swizzle), or of 32 when at most 32 remain
+  const long long hld = static_cast<long long>(c.G) * c.R16, brows = static_cast<long long>(c.S) * c.N;
+  if (rc == WP_OK) rc = make_map_bf16(&maps.hq, c.H, hld, c.T, hld, 64, kBM);
+  if (rc == WP_OK) rc = make_map(&maps.hq32, WP_BF16, c.H, hld, c.T, hld, 32, kBM, 64);
+  if (rc == WP_OK) rc = make_map_bf16(&maps.b[0], c.B, c.R, brows, c.R, 64, 128);
+  if (rc == WP_OK) rc = make_map(&maps.b32[0], WP_BF16, c.B, c.R, brows, c.R, 32, 128, 64);
+  if (rc != WP_OK) return rc;
+  int pairs = tc_max_pairs(smem, nf4);
+  if (pairs <= 0) return WP_ERR_CUDA;
+  pairs = std::min(pairs, p.total_tiles);
+  return launch_tc_fwd(maps, p, 2 * pairs, smem, stream, nf4);
+}
+
+namespace {
+
 // ------------------------------------------------------------------ backward
 // Workspace of lora_linear_bwd, in order (each region 256-byte aligned):
 //   per group: B_g^T padded to [r_g, Ntot] bf16 | per group: A_g^T

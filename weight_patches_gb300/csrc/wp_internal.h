@@ -56,6 +56,15 @@ struct TcAdapter {
   float s;         // combined scale, fp32
 };
 
+// Rows of many adapters (lora_linear_fwd_multi): the slots present in a 256-row block, each with
+// the tensor-memory lanes its MMAs leave alone (bit i of word i / 32 set: row i of the block is
+// not this slot's).
+struct MultiEntry {
+  int slot;
+  int pad[3];
+  uint32_t off[8];
+};
+
 struct TcAdapter32 {
   int group;
   int rank;
@@ -123,6 +132,12 @@ struct TcParams {
   int swiglu;
   uint16_t* eg;
   long long ld_eg;
+  // rows of many adapters: per 256-row block its entries (ent_ld apart) and the rows that have an
+  // adapter; H~ [T, G m_r16] is complete before the kernel starts
+  const MultiEntry* ent;
+  const int* ent_n;
+  const uint32_t* ent_rows;    // [r_blocks][8], bit set: the row has an adapter
+  int ent_ld, m_r16, m_chunks;
   unsigned long long timeout_ns;
 };
 
@@ -269,7 +284,7 @@ int* tc_status_ptr();
 
 int tc_max_pairs(size_t smem_bytes, bool nf4);
 int launch_tc_fwd(const TcMaps& maps, const TcParams& p, int grid, size_t smem_bytes,
-                  cudaStream_t stream, bool nf4);
+                  cudaStream_t stream, bool nf4);   // p.ent set: the many-adapter form
 int tc_fwd_status(int reset);
 
 // ------------------------------------------------------------------ fp32 CUDA-core path
@@ -509,11 +524,20 @@ struct MultiCall {
   float request_scale;
   uint16_t* H;                           // [T, G R16] bf16: s X A^T
   int* act;                              // [T]: the row's slot, or -1 when it uses no adapter
+  float* srow;                           // [T]: s_t (many rows)
+  MultiEntry* ent;                       // [blocks of 256 rows][ent_ld] (many rows)
+  int* ent_n;
+  uint32_t* ent_rows;
+  int ent_ld;
   const void* bias; int bias_f32;
   void* Y; long long ldy; int y_f32;
   int* status;
   unsigned long long timeout_ns;
 };
+// Many rows: the blocks' entries, H~ (wp_multi_shrink.cu), then the fused forward (wp_tc_fwd.cu)
+int launch_multi_plan(const MultiCall& c, cudaStream_t stream);
+int launch_multi_shrink(const MultiCall& c, cudaStream_t stream);
+int multi_fused(const MultiCall& c, const wp_mat* W, cudaStream_t stream);   // wp_api.cu
 // Few rows (wp_multi_small.cu): H~ a (slot, 16 rank rows) per CTA, then W streamed once with the
 // rows as the MMA's width, K split over a cluster.
 int launch_multi_shrink_small(const MultiCall& c, cudaStream_t stream);

@@ -4,10 +4,10 @@
 //
 // (sglang PR, Motivation: the adapter and its scale belong to the request, so a batch meets
 // many of them.)  The adapters of a layer lie in a bank, one per slot, and every row names its
-// slot on the device.
-//
-// First form: the plain projection in fp32, then H~ = bf16(s X A^T) a warp per rank row, then
-// the second contraction added before the single output rounding.
+// slot on the device.  This file holds the entry point: its checks, its workspace and the choice
+// between the two forms -- a few rows, where the weights' bytes are the work (wp_multi_small.cu),
+// and many (the blocks' slots and H~ in wp_multi_shrink.cu, then the fused forward of wp_tc_fwd.cu
+// with a lane mask per slot).
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -18,67 +18,6 @@
 namespace wp {
 
 namespace {
-
-__device__ __forceinline__ float bf2f(uint32_t h) { return __uint_as_float(h << 16); }
-
-__global__ void __launch_bounds__(256) multi_h_kernel(const MultiCall p) {
-  const int t = blockIdx.x;
-  const int a = p.slot[t];
-  const int lane = threadIdx.x & 31;
-  float s = 0.f;
-  if (a >= 0 && a < p.S) {
-    s = p.scale[a];
-    if (p.row_scale) s = __fmul_rn(s, p.row_scale[t]);
-    s = __fmul_rn(s, p.request_scale);
-  }
-  const uint16_t* x = p.X + static_cast<long long>(t) * p.ldx;
-  for (int j = threadIdx.x >> 5; j < p.G * p.R16; j += 8) {
-    const int g = j / p.R16, r = j - g * p.R16;
-    float h = 0.f;
-    if (s != 0.f && r < p.R) {
-      const uint16_t* ar = p.A + (static_cast<long long>(a) * p.G * p.R + g * p.R + r) * p.K;
-      for (int k = lane; k < p.K; k += 32) h = fmaf(bf2f(x[k]), bf2f(ar[k]), h);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) h += __shfl_xor_sync(0xffffffffu, h, o);
-      h *= s;
-    }
-    if (lane == 0) {
-      uint16_t hb;
-      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(hb) : "f"(h));
-      p.H[static_cast<long long>(t) * p.G * p.R16 + j] = hb;
-    }
-  }
-}
-
-__global__ void __launch_bounds__(256) multi_y_kernel(const MultiCall p, const float* base) {
-  const int t = blockIdx.y;
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= p.N) return;
-  const int a = p.slot[t];
-  float y = 0.f;
-  if (base) y = base[static_cast<long long>(t) * p.N + n];
-  else if (p.bias) y = p.bias_f32 ? static_cast<const float*>(p.bias)[n] : bf2f(static_cast<const uint16_t*>(p.bias)[n]);
-  if (a >= 0 && a < p.S) {
-    const int g = n / (p.N / p.G);
-    const uint16_t* b = p.B + (static_cast<long long>(a) * p.N + n) * p.R;
-    const uint16_t* h = p.H + static_cast<long long>(t) * p.G * p.R16 + g * p.R16;
-    float s = p.scale[a];
-    if (p.row_scale) s = __fmul_rn(s, p.row_scale[t]);
-    if (__fmul_rn(s, p.request_scale) != 0.f) {
-      float d = 0.f;
-      for (int r = 0; r < p.R; ++r) d = fmaf(bf2f(h[r]), bf2f(b[r]), d);
-      y += d;
-    }
-  }
-  const long long o = static_cast<long long>(t) * p.ldy + n;
-  if (p.y_f32) {
-    static_cast<float*>(p.Y)[o] = y;
-  } else {
-    uint16_t yb;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(yb) : "f"(y));
-    static_cast<uint16_t*>(p.Y)[o] = yb;
-  }
-}
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t r256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
@@ -94,6 +33,10 @@ int check(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
   if (bank->rank % 8) return WP_ERR_SHAPE;
   if (X->cols % 8 || (bank->out / bank->n_groups) % 8) return WP_ERR_ALIGN;
   if (X->rows > 0x7FFFFFFFll || X->cols > 0x7FFFFFFFll || bank->out > 0x7FFFFFFFll) return WP_ERR_UNSUPPORTED;
+  // the bank's rows are TMA coordinates
+  if (bank->n_slots * bank->out > 0x7FFFFFFFll - 512 ||
+      static_cast<long long>(bank->n_slots) * bank->n_groups * bank->rank > 0x7FFFFFFFll - 512)
+    return WP_ERR_UNSUPPORTED;
   if (W) {
     if (W->dtype != WP_BF16 && W->dtype != WP_NF4) return WP_ERR_DTYPE;
     if (W->rows <= 0 || W->cols <= 0 || W->ld < W->cols) return WP_ERR_INVALID;
@@ -104,23 +47,26 @@ int check(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
 }
 
 // Rows up to which the weight-streaming kernels take a bf16 weight (or none).
-constexpr int kSmallRows = 512;
+constexpr int kSmallRows = 128;
 bool small_rows(int T, const wp_mat* W) { return T <= kSmallRows && (!W || W->dtype == WP_BF16); }
 
+// H~ [T, G R16] | act [T] (few rows), or s [T] | entries | their counts | rows with an adapter
 struct Layout {
-  size_t h = 0, act = 0, base = 0, fwd = 0, total = 0;
+  size_t act = 0, ent = 0, ent_n = 0, ent_rows = 0, total = 0;
+  int ent_ld = 0;
 };
 
 Layout layout(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
   Layout L;
-  const size_t T = static_cast<size_t>(X->rows);
+  const size_t T = static_cast<size_t>(X->rows), blocks = (T + 255) / 256;
   const size_t r16 = (bank->rank + 15) / 16 * 16;
   L.act = r256(T * bank->n_groups * r16 * 2);
-  L.base = L.act + r256(T * 4);
-  L.total = L.fwd = L.base;
-  if (W && !small_rows(static_cast<int>(T), W)) {
-    L.fwd = L.base + r256(T * bank->out * 4);
-    L.total = L.fwd + r256(lora_workspace_size(WP_OP_FWD, X, W, nullptr, 0));
+  L.total = L.ent = L.act + r256(T * 4);
+  if (!small_rows(static_cast<int>(T < (1u << 30) ? T : (1u << 30)), W)) {
+    L.ent_ld = bank->n_slots < 256 ? bank->n_slots : 256;
+    L.ent_n = L.ent + r256(blocks * L.ent_ld * sizeof(MultiEntry));
+    L.ent_rows = L.ent_n + r256(blocks * 4);
+    L.total = L.ent_rows + r256(blocks * 32);
   }
   return L;
 }
@@ -169,7 +115,7 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
   c.X = static_cast<const uint16_t*>(X->data); c.ldx = X->ld;
   c.A = static_cast<const uint16_t*>(bank->A); c.B = static_cast<const uint16_t*>(bank->B);
   c.scale = bank->scale; c.slot = slot; c.row_scale = row_scale; c.request_scale = rs;
-  c.H = reinterpret_cast<uint16_t*>(ws + L.h);
+  c.H = reinterpret_cast<uint16_t*>(ws);
   c.act = reinterpret_cast<int*>(ws + L.act);
   if (bias) {
     c.bias = bias->data;
@@ -188,31 +134,15 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
     if (rc != WP_OK) return rc;
     return launch_multi_small(c, W ? W->data : nullptr, W ? W->ld : 0, st);
   }
-  const float* base = nullptr;
-  if (W) {
-    const wp_out by{ws + L.base, WP_FP32, X->rows, bank->out, bank->out};
-    rc = lora_linear_fwd(X, W, bias, nullptr, 0, 1.0, &by, ws + L.fwd, L.total - L.fwd, stream);
-    if (rc != WP_OK) return rc;
-    base = reinterpret_cast<const float*>(ws + L.base);
-    c.bias = nullptr;
-  }
-  multi_h_kernel<<<c.T, 256, 0, st>>>(c);
-  for (int t0 = 0; t0 < c.T; t0 += 65535) {
-    MultiCall q = c;
-    q.T = c.T - t0 < 65535 ? c.T - t0 : 65535;
-    q.slot += t0;
-    if (q.row_scale) q.row_scale += t0;
-    q.H += static_cast<long long>(t0) * c.G * c.R16;
-    q.Y = static_cast<char*>(c.Y) + static_cast<long long>(t0) * c.ldy * (c.y_f32 ? 4 : 2);
-    multi_y_kernel<<<dim3((c.N + 255) / 256, q.T), 256, 0, st>>>(
-        q, base ? base + static_cast<long long>(t0) * c.N : nullptr);
-  }
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) {
-    set_last_cuda_error(e);
-    return WP_ERR_CUDA;
-  }
-  return WP_OK;
+  c.srow = reinterpret_cast<float*>(ws + L.act);
+  c.ent = reinterpret_cast<MultiEntry*>(ws + L.ent);
+  c.ent_n = reinterpret_cast<int*>(ws + L.ent_n);
+  c.ent_rows = reinterpret_cast<uint32_t*>(ws + L.ent_rows);
+  c.ent_ld = L.ent_ld;
+  rc = launch_multi_plan(c, st);
+  if (rc == WP_OK) rc = launch_multi_shrink(c, st);
+  if (rc == WP_OK) rc = multi_fused(c, W, st);
+  return rc;
 }
 
 }  // extern "C"

@@ -167,9 +167,13 @@ __device__ __forceinline__ float bias_at(const TcParams& p, int col) {
 
 }  // namespace
 
+// kMulti: the rows belong to many adapters (sglang PR, Motivation: the adapter belongs to the
+// request).  There are no rank items: H~ lies ready, each row's from its own slot, and a tile's
+// second contraction runs over the slots present in its 256 rows, each slot's MMAs leaving the
+// other slots' rows (tensor-memory lanes) alone, so that no operand is copied or masked.
 // kF32: the epilogue also adds FP32 adapters by FFMA (those too wide to ride as bf16
 // pieces); a separate instantiation so that the common kernels do not carry its registers.
-template <bool kNF4, bool kF32>
+template <bool kNF4, bool kF32, bool kMulti>
 __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
     tc_fused_fwd_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcParams p) {
   constexpr int kEpiWarp0 = kNF4 ? 4 : 2;              // first epilogue warp
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
       for (int i = 0; i < R - 1 && c_more && ok; ++i) ok = issue_codes();
       // the operands packed by the kernel launched just before (packed A rows, B pieces,
       // cleared flags) are read only after that kernel has finished
-      if (p.n_ad > 0) grid_dependency_wait();
+      if (kMulti || p.n_ad > 0) grid_dependency_wait();
       const int half = p.htot >> 1;
       ItemIter iter = item_iter_begin(p, pair, npairs);
       Item it;
@@ -381,7 +385,27 @@ __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
           }
           if (!ok) break;
         }
-        if (a1 > a0) {
+        if (kMulti) {
+          // second contraction: per slot of the tile's rows, its rows of B against their H~
+          for (int h = 0; h < nblk && ok; ++h) {
+            const MultiEntry* ent = p.ent + static_cast<long long>(blk0 + h) * p.ent_ld;
+            const int n = p.ent_n[blk0 + h];
+            for (int e = 0; e < n && ok; ++e) {
+              const int b_row = ent[e].slot * p.N + t.g * p.out_g + t.j * kBN + static_cast<int>(cta) * 128;
+              for (int c = 0; c < p.m_chunks; ++c) {
+                const bool narrow = p.m_r16 - 64 * c <= 32;
+                const uint32_t box = narrow ? kATileBytes / 2 : kATileBytes;
+                uint8_t* st;
+                uint32_t fb;
+                if (!(ok = claim(4u * box, st, fb))) break;
+                tma_load_2d_pair_hint(st + h * kATileBytes, narrow ? &maps.hq32 : &maps.hq, t.g * p.m_r16 + 64 * c,
+                                      x_row + h * kPairM, fb, keep);
+                tma_load_2d_pair_hint(st + kXBytes, narrow ? &maps.b32[0] : &maps.b[0], c * 64, b_row, fb, keep);
+                advance();
+              }
+            }
+          }
+        } else if (a1 > a0) {
           // second contraction: H~ of the tile's rows (written by the rank items of its
           // blocks) and B
           if (peek >= p.flag_target) {
@@ -474,12 +498,14 @@ __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
         return true;
       };
       auto give_back = [&]() { mma_commit_pair_mc(&empty[s0], kBothCtas); };
+      if (kMulti) grid_dependency_wait();
       ItemIter iter = item_iter_begin(p, pair, npairs);
       Item it;
       while (next_item(iter, p, pair, npairs, it)) {
         const int a0 = it.rank ? 0 : p.ad_begin[it.t.g];
         const int a1 = it.rank ? 0 : p.ad_begin[it.t.g + 1];
-        if (!it.rank && !(p.has_base || a1 > a0)) continue;   // bias-only tile: no MMA
+        // bias-only tile: no MMA
+        if (!it.rank && !(p.has_base || (kMulti ? p.ent_n[it.m] > 0 : a1 > a0))) continue;
         const int b = kNF4 ? 0 : (count & 1);   // a 4-bit W's tile fills all 512 columns
         if (!(ok = mbar_wait_cluster(&acc_empty[b], use_parity() ^ 1u, abort_flag, tmo, status)))
           break;
@@ -524,6 +550,30 @@ __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
                   mma_bf16_pair(acc_t + h * kBN, ad + h * kHalfStep + 2 * kk, bd + kk * (2048 >> 4), idesc_acc_mn,
                                 (kb | kk) != 0 ? 1u : 0u);
               give_back();
+            }
+          }
+          if (kMulti) {
+            const int blk0 = it.m * kMH, nblk = min(kMH, p.r_blocks - blk0);
+            for (int h = 0; h < nblk && ok; ++h) {
+              const MultiEntry* ent = p.ent + static_cast<long long>(blk0 + h) * p.ent_ld;
+              const int n = p.ent_n[blk0 + h];
+              for (int e = 0; e < n && ok; ++e) {
+                const uint4 m0 = *reinterpret_cast<const uint4*>(ent[e].off);
+                const uint4 m1 = *reinterpret_cast<const uint4*>(ent[e].off + 4);
+                const uint32_t lanes[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+                for (int c = 0; c < p.m_chunks; ++c) {
+                  uint32_t off;
+                  if (!(ok = take(off))) break;
+                  const int kext = min(64, p.m_r16 - 64 * c);
+                  const uint64_t bits = kext <= 32 ? kDescSw64K : kDescSw128K;
+                  const uint64_t ad = bits | (u_x + off + h * kHalfStep), bd = bits | (u_w + off);
+                  // without a base the slot's first MMA starts its rows' sums
+                  for (int kk = 0; kk < kext / 16; ++kk)
+                    mma_bf16_pair_lanes(acc_t + h * kBN, ad + 2 * kk, bd + 2 * kk, idesc_acc,
+                                        (p.has_base || c > 0 || kk > 0) ? 1u : 0u, lanes);
+                  give_back();
+                }
+              }
             }
           }
           bool accum = p.has_base != 0;
@@ -591,7 +641,7 @@ __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
     int count = 0;
     auto use_parity = [&]() -> uint32_t { return static_cast<uint32_t>(kNF4 ? count : (count >> 1)) & 1u; };
     uint32_t sidx = 0;                              // staging chunks issued so far
-    if (p.n_ad > 0) grid_dependency_wait();          // rank items release flags cleared by it
+    if (kMulti || p.n_ad > 0) grid_dependency_wait();   // rank items release flags cleared by it
     ItemIter iter = item_iter_begin(p, pair, npairs);
     Item it;
     while (next_item(iter, p, pair, npairs, it)) {
@@ -701,7 +751,7 @@ __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
       }
       const Tile& t = it.t;
       const int a0 = p.ad_begin[t.g], a1 = p.ad_begin[t.g + 1];
-      const bool any_mma = p.has_base || a1 > a0;
+      const bool any_mma = p.has_base || (kMulti ? p.ent_n[t.m] > 0 : a1 > a0);
       if (!kNF4 && p.resid) {
         // merge: pull this thread's residual rows toward L2 one tile ahead of their use (the
         // first tile's own rows too), so that they land while this tile is drained
@@ -839,6 +889,12 @@ __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
       const bool row_ok = row < p.T;
       const uint32_t acc_t = tmem + (b + h) * kBN;
       const bool res_row = !kNF4 && p.resid && row_ok;   // merges run on the bf16 instantiation
+      // many adapters without a base: a row without an adapter was written by no MMA
+      bool written = true;
+      if (kMulti && !kNF4 && !p.has_base) {
+        const int rib = static_cast<int>(cta) * kBM + row_in_cta;   // row within the 256-row block
+        written = (p.ent_rows[t.m * 8 + (rib >> 5)] >> (rib & 31)) & 1u;
+      }
       uint4 rnext[8], rcur[8];
       if (res_row) load_res(row, 0, 0, rnext);
 #pragma unroll 1
@@ -862,7 +918,7 @@ __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
             uint32_t r[32];
             tmem_ld32(acc_t + lane_base + c * cw + c0, r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = u2f(r[i]);
+            for (int i = 0; i < 32; ++i) v[i] = kMulti && !kNF4 && !written ? 0.f : u2f(r[i]);
             if (h == h_end - 1 && c == nchunk - 1 && sub == cw / 32 - 1) {
               // the accumulator is fully in registers: hand it back to the MMA
               tc_fence_before();
@@ -1071,6 +1127,7 @@ __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
       if (ok && lane == 0) mbar_arrive_remote(wfull_l0 + 8u * stage);
       if (++stage == S) { stage = 0; phase ^= 1; }
     };
+    if (kMulti) grid_dependency_wait();
     ItemIter iter = item_iter_begin(p, pair, npairs);
     Item it;
     while (ok && next_item(iter, p, pair, npairs, it)) {
@@ -1125,6 +1182,11 @@ __global__ void __launch_bounds__(kNF4 ? kTcThreadsNF4 : kTcThreads, 1)
       if (!ok) break;
       for (int a = a0; a < a1 && ok; ++a)
         for (int c = 0; c < p.ad[a].nchunks && ok; ++c) pass();
+      if (kMulti) {
+        int steps = 0;
+        for (int blk = it.m * kMH; blk < min((it.m + 1) * kMH, p.r_blocks); ++blk) steps += p.ent_n[blk];
+        for (int i = steps * p.m_chunks; i > 0 && ok; --i) pass();
+      }
     }
   }
 
@@ -1166,7 +1228,7 @@ cudaLaunchConfig_t pair_config(int grid, size_t smem_bytes, cudaStream_t stream,
 
 template <bool kNF4>
 int max_pairs_impl(size_t smem_bytes) {
-  cudaError_t e = cudaFuncSetAttribute(tc_fused_fwd_kernel<kNF4, false>,
+  cudaError_t e = cudaFuncSetAttribute(tc_fused_fwd_kernel<kNF4, false, false>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) {
     set_last_cuda_error(e);
@@ -1175,7 +1237,7 @@ int max_pairs_impl(size_t smem_bytes) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pair_config<kNF4>(2 * 256, smem_bytes, nullptr, attr);
   int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, tc_fused_fwd_kernel<kNF4, false>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&n, tc_fused_fwd_kernel<kNF4, false, false>, &cfg);
   if (e != cudaSuccess || n <= 0) {
     if (e != cudaSuccess) set_last_cuda_error(e);
     n = device_sm_count() / 2;
@@ -1183,18 +1245,18 @@ int max_pairs_impl(size_t smem_bytes) {
   return n;
 }
 
-template <bool kNF4, bool kF32>
+template <bool kNF4, bool kF32, bool kMulti = false>
 int launch_impl(const TcMaps& maps, const TcParams& p, int grid, size_t smem_bytes,
                 cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(tc_fused_fwd_kernel<kNF4, kF32>,
+  cudaError_t e = cudaFuncSetAttribute(tc_fused_fwd_kernel<kNF4, kF32, kMulti>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) {
     set_last_cuda_error(e);
     return WP_ERR_CUDA;
   }
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = pair_config<kNF4>(grid, smem_bytes, stream, attr, p.n_ad > 0);
-  e = cudaLaunchKernelEx(&cfg, tc_fused_fwd_kernel<kNF4, kF32>, maps, p);
+  cudaLaunchConfig_t cfg = pair_config<kNF4>(grid, smem_bytes, stream, attr, kMulti || p.n_ad > 0);
+  e = cudaLaunchKernelEx(&cfg, tc_fused_fwd_kernel<kNF4, kF32, kMulti>, maps, p);
   if (e != cudaSuccess) {
     set_last_cuda_error(e);
     return WP_ERR_CUDA;
@@ -1231,6 +1293,9 @@ int launch_tc_fwd(const TcMaps& maps, const TcParams& params, int grid, size_t s
     p.step_m = npairs / p.nt_g / p.G;
   }
   const bool f32 = p.n_ad32 > 0;
+  if (p.ent)
+    return nf4 ? launch_impl<true, false, true>(maps, p, grid, smem_bytes, stream)
+               : launch_impl<false, false, true>(maps, p, grid, smem_bytes, stream);
   if (nf4)
     return f32 ? launch_impl<true, true>(maps, p, grid, smem_bytes, stream)
                : launch_impl<true, false>(maps, p, grid, smem_bytes, stream);
