@@ -1918,7 +1918,7 @@ size_t lora_workspace_size(int32_t op, const wp_mat* X, const wp_mat* W,
     MergeLayout L;
     return merge_layout(W, adapters, n_adapters, 1.0, &L) ? L.total : 0;
   }
-  if (op == WP_OP_NORM_BWD) return X ? norm_bwd_workspace(X->rows, X->cols) : 0;
+  if (op == WP_OP_NORM_BWD) return X ? norm_bwd_workspace(X->rows, X->cols, X->dtype == WP_FP32) : 0;
   if (!X || n_adapters < 0 || (n_adapters > 0 && !adapters)) return 0;
   if (op == WP_OP_FWD || op == WP_OP_FWD_GROUPED || op == WP_OP_SWIGLU_FWD) {
     FwdPlan plan;

@@ -549,7 +549,7 @@ unsigned long long device_wait_limit_ns();
 
 // ------------------------------------------------------------------ norms
 // workspace bytes of lora_norm_bwd over [T, C]: a partial row of dw and db per CTA
-size_t norm_bwd_workspace(long long T, long long C);
+size_t norm_bwd_workspace(long long T, long long C, bool f32);
 
 // ------------------------------------------------------------------ NF4 table (host)
 void nf4_codebook_host(float out[16]);
