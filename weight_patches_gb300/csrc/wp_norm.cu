@@ -5,14 +5,16 @@
 //             dx = r (h - mean(h) - xh mean(h xh))       (no mean(h) without a mean)
 //             dw = sum_t dy xh,  db = sum_t dy
 //
-// Both are bound by HBM: a row is read once into registers (kept as loaded, unpacked at each
-// use), its sums are taken there (the squares after the mean is out, so that a large mean costs
-// no digits), and written once.  Forward: short rows a warp each, longer ones a CTA each.
-// Backward: a CTA's threads keep their columns over all of its rows, so the column sums dw and db
-// stay in registers; it takes several rows per turn where a thread has few columns, so that one
-// barrier serves them all and enough loads are in flight.  Each CTA leaves one partial row of dw
-// and db in the workspace, which a second kernel adds in order: no atomics, the same bits each
-// time.
+// Both are bound by HBM.  Rows travel by bulk copies into a ring of row slots in shared memory,
+// several rows ahead, so that the bytes in flight do not depend on how many registers the
+// arithmetic takes; a row is then held in registers, its sums are taken there (the squares after
+// the mean is out, so that a large mean costs no digits), and it is written once.  Rows whose start
+// is not 16-byte aligned travel too: the aligned inside by the copy, the few elements around it
+// by plain loads.  The arithmetic runs on float32 pairs (two operations per instruction).
+// Forward: a CTA works through its rows, one warp where a row is short.  Backward: a CTA's threads
+// keep their columns over all of its rows, so the column sums dw and db stay in registers; each
+// CTA leaves one partial row of them in the workspace, which a second kernel adds in order: no
+// atomics, the same bits each time.
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -36,6 +38,9 @@ struct NormParams {
   float eps;
   float inv_c;
   float* part;                     // backward: [gridDim.x][2][C] partial dw, db (may be null)
+  int stages, slot;                // the CTA's ring of rows: stages, bytes of a row's slot
+  int* status;
+  unsigned long long timeout_ns;
 };
 
 __device__ __forceinline__ float bf2f(uint32_t h) { return __uint_as_float(h << 16); }
@@ -114,116 +119,447 @@ __device__ __forceinline__ void load_vec(const void* p, int f32, int vec, int c,
     v[k] = f32 ? __ldg(static_cast<const float*>(p) + c + k) : bf2f(__ldg(static_cast<const unsigned short*>(p) + c + k));
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// Sums of N values over the CTA: red holds N per warp and is not used by the sum before (the
-// callers alternate two).
+// Sums of N values (a power of two) over the CTA; red holds N per warp and is not used by the sum
+// before (the callers alternate two).  A CTA barrier; `fail` becomes whether any thread passed it
+// true.  Within a warp the lanes share the values out as they add (each step halves what a lane
+// still carries), so N values cost N - 1 shuffles and the steps left, not 5 N; across the warps each
+// group of N lanes adds its share of the warps' sums, and the groups meet by shuffles.
 template <int N>
-__device__ __forceinline__ void cta_sum(float (&v)[N], float* red) {
-  const int warps = blockDim.x >> 5;
+__device__ __forceinline__ void cta_sum(float (&v)[N], float* red, bool& fail) {
+  constexpr int kLog = N == 1 ? 0 : N == 2 ? 1 : N == 4 ? 2 : 3;
+  static_assert(N == 1 << kLog, "1, 2, 4 or 8 values");
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (warps == 1) return;
-  if ((threadIdx.x & 31) == 0)
+  for (int b = 0; b < kLog; ++b) {
+    const int o = 16 >> b, half = N >> (b + 1);
+    const bool up = (lane & o) != 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[(threadIdx.x >> 5) * N + i] = v[i];
-  __syncthreads();
+    for (int k = 0; k < half; ++k) {
+      const float give = up ? v[k] : v[k + half], keep = up ? v[k + half] : v[k];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int w = 0; w < warps; ++w)
+  for (int o = 16 >> kLog; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  // lane l holds value l >> (5 - kLog) of its warp
+  if (warps == 1) {
+    fail = __any_sync(0xffffffffu, fail);
+    const float t = v[0];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += red[w * N + i];
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, t, i << (5 - kLog));
+    return;
+  }
+  if ((lane & ((32 >> kLog) - 1)) == 0) red[(threadIdx.x >> 5) * N + (lane >> (5 - kLog))] = v[0];
+  fail = __syncthreads_or(fail);
+  float t = 0.f;
+  for (int w = lane >> kLog; w < warps; w += 32 >> kLog) t += red[w * N + (lane & (N - 1))];
+#pragma unroll
+  for (int o = 16; o >= N; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = N == 1 ? t : __shfl_sync(0xffffffffu, t, i);
 }
 
 constexpr int kMaxThreads = 512;
+constexpr int kMaxStages = 8;
+constexpr int kSmemPerSm = 220 * 1024;
 
-// One row: its raw elements in x, thread `lane` of `tpr` holding vectors lane, lane + tpr, ...
-template <typename T, int V, int NV, bool kWarp>
-__device__ __forceinline__ void fwd_row(const NormParams& p, bool layer, long long row, int lane, int tpr, float* red) {
-  const T* xr = static_cast<const T*>(p.x) + row * p.ldx;
-  Raw<T, V> x[NV];
+// f32x2: two float32 operations in one instruction
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_get(F2 a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// A thread's columns come in chunks: one vector of V elements, or (V = 1) the two elements of
+// vectors 2 i and 2 i + 1; a chunk's values are pairs.
+template <int V>
+struct Chunk {
+  static constexpr int kPairs = V > 1 ? V / 2 : 1;
+  F2 p[kPairs];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + lane) * V;
-    if (c < p.C) x[i].load(xr + c);
-    else x[i].zero();
+    for (int k = 0; k < kPairs; ++k) p[k] = f2(0.f, 0.f);
   }
-  float mu = 0.f;
-  if (layer) {
-    float s[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < V; ++k) s[0] += x[i].at(k);
-    if constexpr (kWarp) s[0] = warp_sum(s[0]);
-    else cta_sum<1>(s, red);
-    mu = s[0] * p.inv_c;
+};
+// first column of chunk i, and of its second element when V = 1
+template <int V>
+__device__ __forceinline__ int chunk_col(int i) {
+  return V > 1 ? (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V
+               : 2 * i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+}
+
+__device__ __forceinline__ float f2_sum(F2 a) {
+  float x, y;
+  f2_get(a, x, y);
+  return x + y;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// A row's 16-byte aligned inside, which travels by bulk copy into a slot at the same offset from a
+// 16-byte boundary; its first `head` and last `tail` elements (none in an aligned row) are read
+// from global memory by the threads that use them.
+template <typename T, int V>
+struct RowSpan {
+  const T* row;
+  int off;                               // elements from the slot's start to the row's
+  int lo, hi;                            // columns [lo, hi) are in the slot
+  __device__ __forceinline__ RowSpan(const T* r, int C) : row(r) {
+    if (V > 1) {                         // aligned rows of whole vectors
+      off = lo = 0;
+      hi = C;
+      return;
+    }
+    const uintptr_t b = reinterpret_cast<uintptr_t>(r), e = b + static_cast<uintptr_t>(C) * sizeof(T);
+    off = static_cast<int>((b & 15u) / sizeof(T));
+    const uintptr_t ab = (b + 15) & ~static_cast<uintptr_t>(15), ae = e & ~static_cast<uintptr_t>(15);
+    lo = ae > ab ? static_cast<int>((ab - b) / sizeof(T)) : C;
+    hi = ae > ab ? static_cast<int>((ae - b) / sizeof(T)) : C;
   }
-  float ss[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if ((i * tpr + lane) * V < p.C)
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float d = x[i].at(k) - mu;
-        ss[0] = fmaf(d, d, ss[0]);
-      }
-  if constexpr (kWarp) ss[0] = warp_sum(ss[0]);
-  else cta_sum<1>(ss, red + 32);
-  const float r = 1.0f / sqrtf(ss[0] * p.inv_c + p.eps);
-  if (p.stats && lane == 0) {
-    p.stats[row] = mu;
-    p.stats[p.T + row] = r;
+};
+
+// The CTA's ring of row slots: stage s holds ROWS rows of each of OPS matrices.  Thread 0 fills a
+// stage with bulk copies; a stage may be filled again once every thread has read it (the callers
+// pass a CTA barrier in between).
+template <typename T, int V, int ROWS, int OPS>
+struct RowRing {
+  uint8_t* base;
+  uint64_t* full;
+  int stages, slot, C;                   // slot: bytes of one row's slot
+  long long T_;
+  __device__ __forceinline__ T* at(int s, int j, int o) const {
+    return reinterpret_cast<T*>(base + ((s * OPS + o) * ROWS + j) * slot);
   }
-  T* yr = static_cast<T*>(p.y) + row * p.ldy;
+  // the rows from r0 into stage s; false when there are none
+  __device__ __forceinline__ bool fill(int s, long long r0, const T* const (&m)[OPS], const long long (&ld)[OPS]) const {
+    if (r0 >= T_) return false;
+    const int rows = T_ - r0 < ROWS ? static_cast<int>(T_ - r0) : ROWS;
+    uint32_t bytes = 0;
+    if (V > 1) {
+      bytes = static_cast<uint32_t>(rows * OPS * C) * sizeof(T);
+    } else {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + lane) * V;
-    if (c < p.C) {
-      float o[V], q[V];
+      for (int j = 0; j < ROWS; ++j)
+        if (j < rows)
 #pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = (x[i].at(k) - mu) * r;
-      if (p.w) {
-        load_vec<V>(p.w, p.w_f32, p.w_vec, c, q);
+          for (int o = 0; o < OPS; ++o) {
+            const RowSpan<T, V> q(m[o] + (r0 + j) * ld[o], C);
+            bytes += static_cast<uint32_t>(q.hi - q.lo) * sizeof(T);
+          }
+    }
+    mbar_arrive_expect_tx(&full[s], bytes);
 #pragma unroll
-        for (int k = 0; k < V; ++k) o[k] *= q[k];
+    for (int o = 0; o < OPS; ++o) {
+      if (V > 1 && ld[o] == C) {           // whole rows one after another: one copy
+        bulk_load(at(s, 0, o), m[o] + r0 * ld[o], static_cast<uint32_t>(rows * C) * sizeof(T), &full[s]);
+        continue;
       }
-      if (p.b) {
-        load_vec<V>(p.b, p.b_f32, p.b_vec, c, q);
 #pragma unroll
-        for (int k = 0; k < V; ++k) o[k] += q[k];
-      }
-      store_row<T, V>(yr + c, o);
+      for (int j = 0; j < ROWS; ++j)
+        if (j < rows) {
+          const RowSpan<T, V> q(m[o] + (r0 + j) * ld[o], C);
+          if (q.hi > q.lo)
+            bulk_load(at(s, j, o) + q.off + q.lo, q.row + q.lo, static_cast<uint32_t>(q.hi - q.lo) * sizeof(T), &full[s]);
+        }
+    }
+    return true;
+  }
+};
+
+// A CTA's walk over its turns: rows, stage and the stage's phase.
+template <int ROWS>
+struct Turn {
+  long long row, step;                   // the turn's first row; rows between turns
+  int s;
+  uint32_t phase;
+  __device__ __forceinline__ Turn() : row(static_cast<long long>(blockIdx.x) * ROWS),
+                                      step(static_cast<long long>(gridDim.x) * ROWS), s(0), phase(0) {}
+  __device__ __forceinline__ void next(int stages) {
+    row += step;
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// One element of a row in its slot (or, outside the slot's span, in global memory)
+template <typename T>
+__device__ __forceinline__ float slot_at(const T* slot, const RowSpan<T, 1>& q, int c) {
+  if (c < q.lo || c >= q.hi) {
+    Raw<T, 1> r;
+    r.load(q.row + c);
+    return r.at(0);
+  }
+  if constexpr (sizeof(T) == 2) return __uint_as_float(static_cast<uint32_t>(slot[q.off + c]) << 16);
+  else return slot[q.off + c];
+}
+
+// Chunk i of a row, as loaded (V > 1: the raw vector; V = 1: two floats), and its values.  The
+// chunk's first column exists; a missing second element (V = 1) is zero.
+template <typename T, int V>
+struct RawChunk {
+  static constexpr int kWords = V > 1 ? 4 : 2;
+  uint32_t u[kWords];
+  __device__ __forceinline__ void load(const T* slot, const RowSpan<T, V>& q, int c, int C) {
+    if constexpr (V > 1) {
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                   : "r"(smem_u32(slot) + static_cast<uint32_t>(c) * static_cast<uint32_t>(sizeof(T))));
+    } else {
+      const int c1 = c + static_cast<int>(blockDim.x);
+      u[0] = __float_as_uint(slot_at(slot, q, c));
+      u[1] = c1 < C ? __float_as_uint(slot_at(slot, q, c1)) : 0u;
+    }
+  }
+  __device__ __forceinline__ Chunk<V> values() const {
+    Chunk<V> o;
+#pragma unroll
+    for (int k = 0; k < Chunk<V>::kPairs; ++k) {
+      if constexpr (V == 8) o.p[k] = f2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
+      else o.p[k] = f2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1]));
+    }
+    return o;
+  }
+};
+
+// The chunk at column c of a weight or bias vector (zero where there is no column)
+template <int V>
+__device__ __forceinline__ Chunk<V> vec_chunk(const void* p, int f32, int vec, int c, int C) {
+  Chunk<V> o;
+  if constexpr (V > 1) {
+    float t[V];
+    load_vec<V>(p, f32, vec, c, t);
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) o.p[k] = f2(t[2 * k], t[2 * k + 1]);
+  } else {
+    float a[1], b[1] = {0.f};
+    const int c1 = c + static_cast<int>(blockDim.x);
+    load_vec<1>(p, f32, 0, c, a);
+    if (c1 < C) load_vec<1>(p, f32, 0, c1, b);
+    o.p[0] = f2(a[0], b[0]);
+  }
+  return o;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_chunk(T* row, const Chunk<V>& x, int c, int C) {
+  if constexpr (V > 1) {
+    float o[V];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) f2_get(x.p[k], o[2 * k], o[2 * k + 1]);
+    store_row<T, V>(row + c, o);
+  } else {
+    float a[1], b[1];
+    f2_get(x.p[0], a[0], b[0]);
+    const int c1 = c + static_cast<int>(blockDim.x);
+    store_row<T, 1>(row + c, a);
+    if (c1 < C) store_row<T, 1>(row + c1, b);
+  }
+}
+
+// A chunk of the partial column sums (rows of C floats, of any alignment)
+template <int V>
+__device__ __forceinline__ void store_sums(float* row, const Chunk<V>& x, int c, int C) {
+#pragma unroll
+  for (int k = 0; k < Chunk<V>::kPairs; ++k) {
+    float a, b;
+    f2_get(x.p[k], a, b);
+    const int c1 = V > 1 ? c + 2 * k + 1 : c + static_cast<int>(blockDim.x);
+    row[V > 1 ? c + 2 * k : c] = a;
+    if (c1 < C) row[c1] = b;
+  }
+}
+
+// Set up the ring: barriers, then the first `stages` turns on their way.
+template <typename T, int V, int ROWS, int OPS>
+__device__ __forceinline__ void ring_begin(RowRing<T, V, ROWS, OPS>& ring, const T* const (&m)[OPS],
+                                           const long long (&ld)[OPS], volatile int* abort_flag) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ring.stages; ++s) mbar_init(&ring.full[s], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    Turn<ROWS> t;
+    for (int s = 0; s < ring.stages; ++s, t.next(ring.stages)) ring.fill(s, t.row, m, ld);
+  }
+  __syncthreads();
+}
+
+// After an expired wait: the copies still in flight land before the CTA leaves (this turn's and
+// those of the stages - 1 turns after it).
+template <typename T, int V, int ROWS, int OPS>
+__device__ __forceinline__ void ring_settle(const RowRing<T, V, ROWS, OPS>& ring, Turn<ROWS> t) {
+  if (threadIdx.x != 0) return;
+  for (int k = 0; k < ring.stages && t.row < ring.T_; ++k, t.next(ring.stages)) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(smem_u32(&ring.full[t.s]), t.phase) && globaltimer_ns() - t0 < 100000000ull) {
     }
   }
 }
 
-// Short rows: a warp each, 8 warps per CTA.
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(256) norm_fwd_warp_kernel(const NormParams p, const bool layer) {
-  const long long stride = static_cast<long long>(gridDim.x) * 8;
-  for (long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < p.T; row += stride)
-    fwd_row<T, V, NV, true>(p, layer, row, threadIdx.x & 31, 32, nullptr);
-}
-
-// Longer rows: a CTA each.
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(kMaxThreads) norm_fwd_cta_kernel(const NormParams p, const bool layer) {
-  __shared__ float red[64];
-  for (long long row = blockIdx.x; row < p.T; row += gridDim.x) {
-    fwd_row<T, V, NV, false>(p, layer, row, threadIdx.x, blockDim.x, red);
-    __syncthreads();                     // the sums are read before the next row's are written
+// The chunks of a weight or bias vector that a thread's columns need; kHold: kept in registers for
+// all rows, else loaded again at each use (where they would not fit beside the row).
+template <int V, int NC, bool kHold>
+struct Held {
+  Chunk<V> c[kHold ? NC : 1];
+  const void* p;
+  int f32, vec, C;
+  __device__ __forceinline__ Held(const void* p_, int f32_, int vec_, int C_) : p(p_), f32(f32_), vec(vec_), C(C_) {
+    if (kHold && p)
+#pragma unroll
+      for (int i = 0; i < (kHold ? NC : 1); ++i) {
+        c[i].zero();
+        if (chunk_col<V>(i) < C) c[i] = vec_chunk<V>(p, f32, vec, chunk_col<V>(i), C);
+      }
   }
+  __device__ __forceinline__ Chunk<V> at(int i) const {
+    return kHold ? c[kHold ? i : 0] : vec_chunk<V>(p, f32, vec, chunk_col<V>(i), C);
+  }
+};
+
+// Forward, ROWS rows of a CTA per turn (a CTA is one warp where that is enough); NC chunks a thread.
+template <typename T, int V, int NC, int ROWS, bool kHold>
+__global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams p, const bool layer) {
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  __shared__ float red[2][16 * ROWS];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ int abort_word;
+  constexpr int P = Chunk<V>::kPairs;
+  const T* const m[1] = {static_cast<const T*>(p.x)};
+  const long long ld[1] = {p.ldx};
+  RowRing<T, V, ROWS, 1> ring{ring_mem, full, p.stages, p.slot, p.C, p.T};
+  ring_begin(ring, m, ld, &abort_word);
+  const Held<V, NC, kHold> w(p.w, p.w_f32, p.w_vec, p.C), b(p.b, p.b_f32, p.b_vec, p.C);
+  bool fail = false;
+  Turn<ROWS> turn;
+  int odd = 0;
+  for (; turn.row < p.T; turn.next(p.stages)) {
+    const int rows = p.T - turn.row < ROWS ? static_cast<int>(p.T - turn.row) : ROWS;
+    fail = !mbar_wait(&full[turn.s], turn.phase, &abort_word, p.timeout_ns, p.status);
+    Chunk<V> x[ROWS][NC];
+    float sum[ROWS], mu[ROWS];
+    F2 t[ROWS];
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      t[j] = f2(0.f, 0.f);
+      mu[j] = 0.f;
+      const RowSpan<T, V> q(m[0] + (turn.row + j) * p.ldx, p.C);
+      const T* slot = ring.at(turn.s, j, 0);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int c = chunk_col<V>(i);
+        if (c < p.C && j < rows) {
+          RawChunk<T, V> r;
+          r.load(slot, q, c, p.C);
+          x[j][i] = r.values();
+        } else {
+          x[j][i].zero();
+        }
+      }
+    }
+    if (layer) {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int k = 0; k < P; ++k) t[j] = f2_add(t[j], x[j][i].p[k]);
+        sum[j] = f2_sum(t[j]);
+        t[j] = f2(0.f, 0.f);
+      }
+      cta_sum<ROWS>(sum, red[odd], fail);
+      odd ^= 1;
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        mu[j] = sum[j] * p.inv_c;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int c = chunk_col<V>(i);
+          if (c < p.C) {
+            const F2 nm = f2(-mu[j], V == 1 && c + static_cast<int>(blockDim.x) >= p.C ? 0.f : -mu[j]);
+#pragma unroll
+            for (int k = 0; k < P; ++k) x[j][i].p[k] = f2_add(x[j][i].p[k], nm);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int k = 0; k < P; ++k) t[j] = f2_fma(x[j][i].p[k], x[j][i].p[k], t[j]);
+      sum[j] = f2_sum(t[j]);
+    }
+    cta_sum<ROWS>(sum, red[odd], fail);  // every thread has read the stage; `fail` is now the CTA's
+    odd ^= 1;
+    if (threadIdx.x == 0 && !fail) ring.fill(turn.s, turn.row + turn.step * p.stages, m, ld);
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      sum[j] = 1.0f / sqrtf(sum[j] * p.inv_c + p.eps);
+      if (p.stats && threadIdx.x == 0 && j < rows) {
+        p.stats[turn.row + j] = mu[j];
+        p.stats[p.T + turn.row + j] = sum[j];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = chunk_col<V>(i);
+      if (c < p.C) {
+        Chunk<V> wc, bc;
+        if (p.w) wc = w.at(i);
+        if (p.b) bc = b.at(i);
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+          if (j >= rows) continue;
+          const F2 rr = f2(sum[j], sum[j]);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            x[j][i].p[k] = f2_mul(x[j][i].p[k], rr);
+            if (p.w) x[j][i].p[k] = f2_mul(x[j][i].p[k], wc.p[k]);
+            if (p.b) x[j][i].p[k] = f2_add(x[j][i].p[k], bc.p[k]);
+          }
+          store_chunk<T, V>(static_cast<T*>(p.y) + (turn.row + j) * p.ldy, x[j][i], c, p.C);
+        }
+      }
+    }
+    if (fail) break;
+  }
+  if (fail) ring_settle(ring, turn);
 }
 
 // Rows too long for the registers of 512 threads: three passes over the row.
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) norm_fwd_long_kernel(const NormParams p, const bool layer) {
   __shared__ float red[64];
+  bool none = false;
   for (long long row = blockIdx.x; row < p.T; row += gridDim.x) {
     const T* xr = static_cast<const T*>(p.x) + row * p.ldx;
     float mu = 0.f;
@@ -234,7 +570,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_long_kernel(const NormPa
         v.load(xr + c);
         s[0] += v.at(0);
       }
-      cta_sum<1>(s, red);
+      cta_sum<1>(s, red, none);
       mu = s[0] * p.inv_c;
     }
     float ss[1] = {0.f};
@@ -242,7 +578,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_long_kernel(const NormPa
       v.load(xr + c);
       ss[0] = fmaf(v.at(0) - mu, v.at(0) - mu, ss[0]);
     }
-    cta_sum<1>(ss, red + 32);
+    cta_sum<1>(ss, red + 32, none);
     const float r = 1.0f / sqrtf(ss[0] * p.inv_c + p.eps);
     if (p.stats && threadIdx.x == 0) {
       p.stats[row] = mu;
@@ -266,98 +602,142 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_long_kernel(const NormPa
   }
 }
 
-// ROWS rows of a CTA per turn: thread t holds vectors t, t + blockDim, ... of each.
-template <typename T, int V, int NV, int ROWS>
+// Backward, ROWS rows of a CTA per turn; NC chunks a thread.  Between the sums and dx a thread keeps
+// xh and h of its columns, or (kRaw, where those and dw, db would not fit its registers) the raw
+// elements, and forms them again.
+template <typename T, int V, int NC, int ROWS, bool kRaw, bool kHold>
 __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams p, const bool layer) {
+  extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[2][16 * 2 * ROWS];
-  const int lane = threadIdx.x, tpr = blockDim.x;
-  float dw[NV][V], db[NV][V];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ int abort_word;
+  constexpr int P = Chunk<V>::kPairs;
+  const T* const m[2] = {static_cast<const T*>(p.x), static_cast<const T*>(p.dy)};
+  const long long ld[2] = {p.ldx, p.lddy};
+  RowRing<T, V, ROWS, 2> ring{ring_mem, full, p.stages, p.slot, p.C, p.T};
+  ring_begin(ring, m, ld, &abort_word);
+  Chunk<V> dw[NC], db[NC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < V; ++k) dw[i][k] = db[i][k] = 0.f;
-  int turn = 0;
-  for (long long row0 = static_cast<long long>(blockIdx.x) * ROWS; row0 < p.T;
-       row0 += static_cast<long long>(gridDim.x) * ROWS, turn ^= 1) {
-    Raw<T, V> x[ROWS][NV], g[ROWS][NV];
-    float mu[ROWS], r[ROWS], s[2 * ROWS];
+  for (int i = 0; i < NC; ++i) {
+    dw[i].zero();
+    db[i].zero();
+  }
+  const Held<V, NC, kHold> wh(p.w, p.w_f32, p.w_vec, p.C);
+  bool fail = false;
+  Turn<ROWS> turn;
+  int odd = 0;
+  // the rows' mu and r, read a turn ahead
+  float mu_n[ROWS], r_n[ROWS];
+  auto stats_of = [&](long long row0) {
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      const long long row = row0 + j;
-      const bool ok = row < p.T;
-      const T* xr = static_cast<const T*>(p.x) + (ok ? row : 0) * p.ldx;
-      const T* gr = static_cast<const T*>(p.dy) + (ok ? row : 0) * p.lddy;
-      mu[j] = layer && ok ? __ldg(p.stats + row) : 0.f;
-      r[j] = ok ? __ldg(p.stats + p.T + row) : 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + lane) * V;
-        if (ok && c < p.C) {
-          x[j][i].load(xr + c);
-          g[j][i].load(gr + c);
-        } else {
-          x[j][i].zero();
-          g[j][i].zero();
-        }
-      }
+      const bool ok = row0 + j < p.T;
+      mu_n[j] = layer && ok ? __ldg(p.stats + row0 + j) : 0.f;
+      r_n[j] = ok ? __ldg(p.stats + p.T + row0 + j) : 0.f;
     }
-    float w[V];
+  };
+  stats_of(turn.row);
+  for (; turn.row < p.T; turn.next(p.stages), odd ^= 1) {
+    const long long row0 = turn.row;
+    const int s = turn.s;
+    const int rows = p.T - row0 < ROWS ? static_cast<int>(p.T - row0) : ROWS;
+    F2 nm[ROWS], rr[ROWS], s1[ROWS], s2[ROWS];
 #pragma unroll
-    for (int k = 0; k < 2 * ROWS; ++k) s[k] = 0.f;
+    for (int j = 0; j < ROWS; ++j) {
+      nm[j] = f2(-mu_n[j], -mu_n[j]);
+      rr[j] = f2(r_n[j], r_n[j]);
+      s1[j] = s2[j] = f2(0.f, 0.f);
+    }
+    stats_of(row0 + turn.step);
+    fail = !mbar_wait(&full[s], turn.phase, &abort_word, p.timeout_ns, p.status);
+    Chunk<V> x[ROWS][kRaw ? 1 : NC], h[ROWS][kRaw ? 1 : NC];     // xh and dy w
+    RawChunk<T, V> rx[ROWS][kRaw ? NC : 1], rg[ROWS][kRaw ? NC : 1];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + lane) * V;
+    for (int i = 0; i < NC; ++i) {
+      const int c = chunk_col<V>(i);
       if (c < p.C) {
-        if (p.w) load_vec<V>(p.w, p.w_f32, p.w_vec, c, w);
+        Chunk<V> w;
+        if (p.w) w = wh.at(i);
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j)
-          if (row0 + j < p.T)
+        for (int j = 0; j < ROWS; ++j) {
+          if (j >= rows) continue;
+          RawChunk<T, V> a, g;
+          a.load(ring.at(s, j, 0), RowSpan<T, V>(m[0] + (row0 + j) * ld[0], p.C), c, p.C);
+          g.load(ring.at(s, j, 1), RowSpan<T, V>(m[1] + (row0 + j) * ld[1], p.C), c, p.C);
+          if (kRaw) {
+            rx[j][i] = a;
+            rg[j][i] = g;
+          }
+          Chunk<V> xh = a.values(), hh = g.values();
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-              const float xh = (x[j][i].at(k) - mu[j]) * r[j], gk = g[j][i].at(k);
-              dw[i][k] = fmaf(gk, xh, dw[i][k]);
-              db[i][k] += gk;
-              const float h = p.w ? gk * w[k] : gk;
-              s[2 * j] += h;
-              s[2 * j + 1] = fmaf(h, xh, s[2 * j + 1]);
-            }
-      }
-    }
-    if (p.y) {
-      cta_sum<2 * ROWS>(s, red[turn]);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + lane) * V;
-        if (c < p.C) {
-          if (p.w) load_vec<V>(p.w, p.w_f32, p.w_vec, c, w);
-#pragma unroll
-          for (int j = 0; j < ROWS; ++j)
-            if (row0 + j < p.T) {
-              const float m1 = layer ? s[2 * j] * p.inv_c : 0.f, m2 = s[2 * j + 1] * p.inv_c;
-              float o[V];
-#pragma unroll
-              for (int k = 0; k < V; ++k) {
-                const float xh = (x[j][i].at(k) - mu[j]) * r[j];
-                const float h = p.w ? g[j][i].at(k) * w[k] : g[j][i].at(k);
-                o[k] = r[j] * (h - m1 - xh * m2);
-              }
-              store_row<T, V>(static_cast<T*>(p.y) + (row0 + j) * p.ldy + c, o);
-            }
+          for (int k = 0; k < P; ++k) {
+            xh.p[k] = f2_mul(f2_add(xh.p[k], nm[j]), rr[j]);
+            dw[i].p[k] = f2_fma(hh.p[k], xh.p[k], dw[i].p[k]);
+            db[i].p[k] = f2_add(db[i].p[k], hh.p[k]);
+            if (p.w) hh.p[k] = f2_mul(hh.p[k], w.p[k]);
+            s1[j] = f2_add(s1[j], hh.p[k]);
+            s2[j] = f2_fma(hh.p[k], xh.p[k], s2[j]);
+          }
+          if (!kRaw) {
+            x[j][i] = xh;
+            h[j][i] = hh;
+          }
         }
       }
     }
+    float sums[2 * ROWS];
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      sums[2 * j] = f2_sum(s1[j]);
+      sums[2 * j + 1] = f2_sum(s2[j]);
+    }
+    cta_sum<2 * ROWS>(sums, red[odd], fail);   // every thread has read the stage; `fail` is the CTA's
+    if (threadIdx.x == 0 && !fail) ring.fill(turn.s, turn.row + turn.step * p.stages, m, ld);
+    if (p.y) {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        if (j >= rows) continue;
+        const float m1 = layer ? sums[2 * j] * p.inv_c : 0.f, m2 = sums[2 * j + 1] * p.inv_c;
+        const F2 a = f2(-m1, -m1), b = f2(-m2, -m2);
+        T* yr = static_cast<T*>(p.y) + (row0 + j) * p.ldy;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int c = chunk_col<V>(i);
+          if (c < p.C) {
+            Chunk<V> xh, hh;
+            if (kRaw) {
+              xh = rx[j][i].values();
+              hh = rg[j][i].values();
+              Chunk<V> w;
+              if (p.w) w = wh.at(i);
+#pragma unroll
+              for (int k = 0; k < P; ++k) {
+                xh.p[k] = f2_mul(f2_add(xh.p[k], nm[j]), rr[j]);
+                if (p.w) hh.p[k] = f2_mul(hh.p[k], w.p[k]);
+              }
+            } else {
+              xh = x[j][i];
+              hh = h[j][i];
+            }
+#pragma unroll
+            for (int k = 0; k < P; ++k) xh.p[k] = f2_mul(f2_fma(xh.p[k], b, f2_add(hh.p[k], a)), rr[j]);
+            store_chunk<T, V>(yr, xh, c, p.C);
+          }
+        }
+      }
+    }
+    if (fail) break;
   }
+  if (fail) ring_settle(ring, turn);
   if (!p.part) return;
   float* out = p.part + static_cast<long long>(blockIdx.x) * 2 * p.C;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + lane) * V;
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (c + k < p.C) {
-        out[c + k] = dw[i][k];
-        out[p.C + c + k] = db[i][k];
-      }
+  for (int i = 0; i < NC; ++i) {
+    const int c = chunk_col<V>(i);
+    if (c < p.C) {
+      store_sums<V>(out, dw[i], c, p.C);
+      store_sums<V>(out + p.C, db[i], c, p.C);
+    }
   }
 }
 
@@ -367,6 +747,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams 
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) norm_bwd_long_kernel(const NormParams p, const bool layer) {
   __shared__ float red[32];
+  bool none = false;
   float* out = p.part ? p.part + static_cast<long long>(blockIdx.x) * 2 * p.C : nullptr;
   if (out)
     for (int c = threadIdx.x; c < p.C; c += kMaxThreads) out[c] = out[p.C + c] = 0.f;
@@ -390,7 +771,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_long_kernel(const NormPa
       s[1] = fmaf(h, xh, s[1]);
     }
     if (p.y) {
-      cta_sum<2>(s, red);
+      cta_sum<2>(s, red, none);
       const float m1 = layer ? s[0] * p.inv_c : 0.f, m2 = s[1] * p.inv_c;
       T* yr = static_cast<T*>(p.y) + row * p.ldy;
       for (int c = threadIdx.x; c < p.C; c += kMaxThreads) {
@@ -442,102 +823,147 @@ bool valid_vec(const wp_mat* v, long long C) {
          v->rows * v->cols == C;
 }
 
+// How a row length is worked on: vectors (or single elements) per thread (0: the long form), rows per turn, threads,
+// CTAs per SM, ring stages and bytes of a row's slot.
+struct Form {
+  int nv, rows, threads, per_sm, stages, slot;
+};
+
 // Threads that share a row: each holds nv vectors of it, a whole number of warps in all.
 int row_threads(long long vectors, int nv) {
   return static_cast<int>(((vectors + nv - 1) / nv + 31) / 32 * 32);
 }
 
-// Form of the backward for rows of C elements: vectors per thread, rows per turn (four where a
-// thread has one vector of each, two for two; the single-element form likewise by elements),
-// threads, and the most CTAs (about 1024 threads' worth per SM, two at least: each leaves a partial
-// row).  nv 0: the long form.
-struct BwdForm {
-  int nv, rows, threads, ctas;
-};
-
-BwdForm bwd_form(long long C, bool f32, bool vec) {
-  const int V = vec ? (f32 ? 4 : 8) : 1;
-  const long long n = C / V;
-  BwdForm f{0, 1, 512, 0};
-  if (vec) {
-    if (n <= 320) f = {1, 4, 0, 0};
-    else if (n <= 384 * 2) f = {2, 2, 0, 0};
-    else if (n <= 512 * 4) f = {4, 1, 0, 0};
-  } else {
-    if (n <= 256 * 2) f = {2, 4, 0, 0};
-    else if (n <= 384 * 8) f = {8, 2, 0, 0};
-    else if (n <= 512 * 16) f = {16, 1, 0, 0};
-    else if (n <= 512 * 28) f = {28, 1, 0, 0};
+// The ring of a form: as many CTAs per SM as 128 registers a thread allow (at most 16), the
+// stages that then fit their shared memory, at most kMaxStages; fewer CTAs when two stages do not.
+bool ring_form(Form* f, long long C, bool f32, bool vec, int ops) {
+  const int size = f32 ? 4 : 2;
+  f->slot = static_cast<int>((C * size + 15) / 16 * 16 + (vec ? 0 : 16));
+  const size_t stage = static_cast<size_t>(f->rows) * ops * f->slot;
+  f->per_sm = kMaxThreads / f->threads;
+  if (f->per_sm > 16) f->per_sm = 16;
+  if (f->per_sm < 1) f->per_sm = 1;
+  for (;; --f->per_sm) {
+    const size_t room = static_cast<size_t>(kSmemPerSm) / f->per_sm - 2048;
+    f->stages = static_cast<int>(room / stage < kMaxStages ? room / stage : kMaxStages);
+    if (f->stages >= 2 || f->per_sm == 1) break;
   }
-  if (f.nv) f.threads = row_threads(n, f.nv);
-  const int per_sm = 1024 / f.threads;
-  f.ctas = (per_sm < 2 ? 2 : (per_sm > 8 ? 8 : per_sm)) * device_sm_count();
+  return f->stages >= 2;
+}
+
+// Forward: 16 or so elements a thread and four rows a turn, so that what a turn costs besides its
+// elements (waits, sums, barriers) is spread over 64; longer rows take more elements and fewer rows.
+Form fwd_form(long long C, bool f32, bool vec) {
+  const long long n = vec ? C / (f32 ? 4 : 8) : C;
+  Form f{0, 1, kMaxThreads, 2, 0, 0};
+  if (C > (1 << 20)) return f;
+  struct { int nv, rows, top; } const vecs[] = {{1, 4, 64}, {2, 4, 512}, {4, 2, 512}, {8, 1, 512}},
+                                      ones[] = {{2, 4, 64}, {8, 4, 384}, {16, 2, 512}, {32, 1, 512}};
+  for (int i = 0; i < 4; ++i) {
+    const auto& q = vec ? vecs[i] : ones[i];
+    if (n <= static_cast<long long>(q.nv) * q.top) {
+      f.nv = q.nv;
+      f.rows = q.rows;
+      f.threads = row_threads(n, q.nv);
+      break;
+    }
+  }
+  if (f.nv && !ring_form(&f, C, f32, vec, 1)) f = Form{0, 1, kMaxThreads, 2, 0, 0};
   return f;
 }
 
-template <typename T, int V, int NV>
-int run_fwd(const NormParams& p, bool layer, cudaStream_t st) {
-  const int threads = row_threads(p.C / V, NV);
-  norm_fwd_cta_kernel<T, V, NV><<<static_cast<unsigned>(p.T < (1 << 30) ? p.T : (1 << 30)), threads, 0, st>>>(p, layer);
-  return last_launch();
-}
-
-template <typename T, int V, int NV>
-int run_fwd_warp(const NormParams& p, bool layer, cudaStream_t st) {
-  const long long need = (p.T + 7) / 8;
-  norm_fwd_warp_kernel<T, V, NV><<<static_cast<unsigned>(need < (1 << 30) ? need : (1 << 30)), 256, 0, st>>>(p, layer);
-  return last_launch();
-}
-
-template <typename T, int V, int NV, int ROWS>
-void run_bwd(const NormParams& p, const BwdForm& f, bool layer, int* grid, cudaStream_t st) {
-  const long long need = (p.T + ROWS - 1) / ROWS;
-  *grid = static_cast<int>(need < f.ctas ? need : f.ctas);
-  norm_bwd_kernel<T, V, NV, ROWS><<<*grid, f.threads, 0, st>>>(p, layer);
-}
-
-// Short rows take a warp each (no barrier); beyond 8 vectors (16 single elements) a lane, a CTA
-// with as few vectors a thread as 256 threads allow.
-template <typename T>
-int dispatch_fwd(const NormParams& p, bool vec, bool layer, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
-  if (vec) {
-    const int n = p.C / V;
-    if (n <= 32) return run_fwd_warp<T, V, 1>(p, layer, st);
-    if (n <= 32 * 4) return run_fwd_warp<T, V, 4>(p, layer, st);
-    if (n <= 32 * 8) return run_fwd_warp<T, V, 8>(p, layer, st);
-    if (n <= 256 * 2) return run_fwd<T, V, 2>(p, layer, st);
-    if (n <= 256 * 4) return run_fwd<T, V, 4>(p, layer, st);
-    if (n <= 512 * 8) return run_fwd<T, V, 8>(p, layer, st);
-  } else {
-    if (p.C <= 32 * 4) return run_fwd_warp<T, 1, 4>(p, layer, st);
-    if (p.C <= 32 * 16) return run_fwd_warp<T, 1, 16>(p, layer, st);
-    if (p.C <= 256 * 8) return run_fwd<T, 1, 8>(p, layer, st);
-    if (p.C <= 512 * 16) return run_fwd<T, 1, 16>(p, layer, st);
-    if (p.C <= 512 * 32) return run_fwd<T, 1, 32>(p, layer, st);
+// Backward: fewer elements a thread (its dw, db, weight, xh and h take registers each).
+Form bwd_form(long long C, bool f32, bool vec) {
+  const long long n = vec ? C / (f32 ? 4 : 8) : C;
+  Form f{0, 1, kMaxThreads, 2, 0, 0};
+  if (C > (1 << 20)) return f;
+  struct { int nv, rows, top; } const vecs[] = {{1, 4, 384}, {2, 1, 384}, {4, 1, 512}, {4, 1, 512}},
+                                      ones[] = {{2, 4, 256}, {8, 2, 288}, {16, 1, 512}, {28, 1, 512}};
+  for (int i = 0; i < 4; ++i) {
+    const auto& q = vec ? vecs[i] : ones[i];
+    if (n <= static_cast<long long>(q.nv) * q.top) {
+      f.nv = q.nv;
+      f.rows = q.rows;
+      f.threads = row_threads(n, q.nv);
+      break;
+    }
   }
-  norm_fwd_long_kernel<T><<<static_cast<unsigned>(p.T < (1 << 30) ? p.T : (1 << 30)), kMaxThreads, 0, st>>>(p, layer);
-  return last_launch();
+  if (f.nv && !ring_form(&f, C, f32, vec, 2)) f = Form{0, 1, kMaxThreads, 2, 0, 0};
+  return f;
+}
+
+template <typename K>
+int launch(K kernel, int blocks, const Form& f, size_t smem, const NormParams& p, bool layer, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
+  if (e == cudaSuccess) {
+    kernel<<<blocks, f.threads, smem, st>>>(p, layer);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) return WP_OK;
+  set_last_cuda_error(e);
+  return WP_ERR_CUDA;
+}
+
+int blocks_of(long long T, const Form& f) {
+  const long long need = (T + f.rows - 1) / f.rows, cap = static_cast<long long>(f.per_sm) * device_sm_count();
+  return static_cast<int>(need < cap ? need : cap);
 }
 
 template <typename T>
-int dispatch_bwd(const NormParams& p, bool vec, bool layer, int* grid, cudaStream_t st) {
+int dispatch_fwd(NormParams p, bool vec, bool layer, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const BwdForm f = bwd_form(p.C, sizeof(T) == 4, vec);
+  const Form f = fwd_form(p.C, sizeof(T) == 4, vec);
   if (f.nv == 0) {
-    *grid = static_cast<int>(p.T < f.ctas ? p.T : f.ctas);
-    norm_bwd_long_kernel<T><<<*grid, kMaxThreads, 0, st>>>(p, layer);
-  } else if (vec) {
-    if (f.nv == 1) run_bwd<T, V, 1, 4>(p, f, layer, grid, st);
-    else if (f.nv == 2) run_bwd<T, V, 2, 2>(p, f, layer, grid, st);
-    else run_bwd<T, V, 4, 1>(p, f, layer, grid, st);
-  } else {
-    if (f.nv == 2) run_bwd<T, 1, 2, 4>(p, f, layer, grid, st);
-    else if (f.nv == 8) run_bwd<T, 1, 8, 2>(p, f, layer, grid, st);
-    else if (f.nv == 16) run_bwd<T, 1, 16, 1>(p, f, layer, grid, st);
-    else run_bwd<T, 1, 28, 1>(p, f, layer, grid, st);
+    const long long cap = 4ll * device_sm_count();
+    norm_fwd_long_kernel<T><<<static_cast<unsigned>(p.T < cap ? p.T : cap), kMaxThreads, 0, st>>>(p, layer);
+    return last_launch();
   }
-  return last_launch();
+  p.stages = f.stages;
+  p.slot = f.slot;
+  const size_t smem = static_cast<size_t>(f.stages) * f.rows * f.slot;
+  const int g = blocks_of(p.T, f);
+  if (vec) {
+    switch (f.nv) {
+      case 1: return launch(norm_fwd_kernel<T, V, 1, 4, true>, g, f, smem, p, layer, st);
+      case 2: return launch(norm_fwd_kernel<T, V, 2, 4, sizeof(T) == 4>, g, f, smem, p, layer, st);
+      case 4: return launch(norm_fwd_kernel<T, V, 4, 2, false>, g, f, smem, p, layer, st);
+      default: return launch(norm_fwd_kernel<T, V, 8, 1, false>, g, f, smem, p, layer, st);
+    }
+  }
+  switch (f.nv) {                        // two elements a chunk
+    case 2: return launch(norm_fwd_kernel<T, 1, 1, 4, true>, g, f, smem, p, layer, st);
+    case 8: return launch(norm_fwd_kernel<T, 1, 4, 4, true>, g, f, smem, p, layer, st);
+    case 16: return launch(norm_fwd_kernel<T, 1, 8, 2, true>, g, f, smem, p, layer, st);
+    default: return launch(norm_fwd_kernel<T, 1, 16, 1, false>, g, f, smem, p, layer, st);
+  }
+}
+
+template <typename T>
+int dispatch_bwd(NormParams p, bool vec, bool layer, int* grid, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const Form f = bwd_form(p.C, sizeof(T) == 4, vec);
+  const int g = *grid = blocks_of(p.T, f);
+  if (f.nv == 0) {
+    norm_bwd_long_kernel<T><<<g, kMaxThreads, 0, st>>>(p, layer);
+    return last_launch();
+  }
+  p.stages = f.stages;
+  p.slot = f.slot;
+  const size_t smem = static_cast<size_t>(f.stages) * f.rows * 2 * f.slot;
+  if (vec) {
+    switch (f.nv) {
+      case 1: return launch(norm_bwd_kernel<T, V, 1, 4, false, true>, g, f, smem, p, layer, st);
+      case 2: return launch(norm_bwd_kernel<T, V, 2, 1, false, true>, g, f, smem, p, layer, st);
+      default: return launch(norm_bwd_kernel<T, V, 4, 1, sizeof(T) == 2, false>, g, f, smem, p, layer, st);
+    }
+  }
+  switch (f.nv) {                        // two elements a chunk
+    case 2: return launch(norm_bwd_kernel<T, 1, 1, 4, false, true>, g, f, smem, p, layer, st);
+    case 8: return launch(norm_bwd_kernel<T, 1, 4, 2, false, true>, g, f, smem, p, layer, st);
+    case 16: return launch(norm_bwd_kernel<T, 1, 8, 1, false, true>, g, f, smem, p, layer, st);
+    default: return launch(norm_bwd_kernel<T, 1, 14, 1, false, false>, g, f, smem, p, layer, st);
+  }
 }
 
 bool valid_rows(const wp_mat* m) {
@@ -550,12 +976,11 @@ bool valid_rows(const wp_mat* m) {
 size_t norm_bwd_workspace(long long T, long long C, bool f32) {
   // a partial row of dw and db for each CTA of either form (16-byte aligned rows or not)
   if (T < 0 || C <= 0) return 0;
-  long long n = bwd_form(C, f32, false).ctas;
+  int n = blocks_of(T, bwd_form(C, f32, false));
   if (C % (f32 ? 4 : 8) == 0) {
-    const long long v = bwd_form(C, f32, true).ctas;
+    const int v = blocks_of(T, bwd_form(C, f32, true));
     if (v > n) n = v;
   }
-  if (T < n) n = T;
   return (static_cast<size_t>(n) * 2 * C * 4 + 255) & ~static_cast<size_t>(255);
 }
 
@@ -588,6 +1013,12 @@ int lora_norm_fwd(const wp_mat* X, const wp_mat* weight, const wp_mat* bias, int
   p.stats = stats;
   p.eps = static_cast<float>(eps);
   p.inv_c = 1.0f / static_cast<float>(p.C);
+  p.timeout_ns = device_wait_limit_ns();
+  p.status = tc_status_ptr();
+  if (!p.status) {
+    set_last_cuda_error(cudaGetLastError());
+    return WP_ERR_CUDA;
+  }
   const int V = X->dtype == WP_BF16 ? 8 : 4;
   const bool vec = p.C % V == 0 && p.ldx % V == 0 && p.ldy % V == 0 && al16(p.x) && al16(p.y);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -639,6 +1070,12 @@ int lora_norm_bwd(const wp_mat* dY, const wp_mat* X, const wp_mat* weight, const
   p.y = dX ? dX->data : nullptr; p.ldy = dX ? dX->ld : 0;
   p.stats = const_cast<float*>(stats);
   p.inv_c = 1.0f / static_cast<float>(p.C);
+  p.timeout_ns = device_wait_limit_ns();
+  p.status = tc_status_ptr();
+  if (!p.status) {
+    set_last_cuda_error(cudaGetLastError());
+    return WP_ERR_CUDA;
+  }
   p.part = sums ? static_cast<float*>(workspace) : nullptr;
   const int V = X->dtype == WP_BF16 ? 8 : 4;
   const bool vec = p.C % V == 0 && p.ldx % V == 0 && p.lddy % V == 0 && al16(p.x) && al16(p.dy) &&
