@@ -163,33 +163,20 @@ constexpr int kMaxThreads = 512;
 constexpr int kMaxStages = 8;
 constexpr int kSmemPerSm = 220 * 1024;
 
-// f32x2: two float32 operations in one instruction
+// Pairs of float32.  (The packed f32x2 instructions halve the arithmetic but cost more in moves that
+// bring unpacked bf16 values into register pairs: 5 integer instructions an element against 3 fp32
+// ones saved, the 1536-wide forward 61 us against 41.)
 struct F2 {
-  unsigned long long v;
+  float x, y;
 };
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
+__device__ __forceinline__ F2 f2(float a, float b) { return F2{a, b}; }
 __device__ __forceinline__ void f2_get(F2 a, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+  x = a.x;
+  y = a.y;
 }
-__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) { return F2{a.x + b.x, a.y + b.y}; }
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) { return F2{a.x * b.x, a.y * b.y}; }
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) { return F2{fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)}; }
 
 // A thread's columns come in chunks: one vector of V elements, or (V = 1) the two elements of
 // vectors 2 i and 2 i + 1; a chunk's values are pairs.
@@ -215,9 +202,8 @@ __device__ __forceinline__ float f2_sum(F2 a) {
   return x + y;
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
@@ -244,81 +230,125 @@ struct RowSpan {
   }
 };
 
-// The CTA's ring of row slots: stage s holds ROWS rows of each of OPS matrices.  Thread 0 fills a
-// stage with bulk copies; a stage may be filled again once every thread has read it (the callers
-// pass a CTA barrier in between).
+// The CTA's walk: turn after turn of ROWS rows, through a ring of stages that each hold those rows
+// of OPS matrices (operand-major slots).  Thread 0 fills a stage with bulk copies; a stage may be
+// filled again once every thread has read it (the callers pass a CTA barrier in between).  Row
+// numbers are 32-bit, offsets 64-bit; pointers step from turn to turn.
 template <typename T, int V, int ROWS, int OPS>
-struct RowRing {
-  uint8_t* base;
+struct Walk {
+  const NormParams& p;
   uint64_t* full;
-  int stages, slot, C;                   // slot: bytes of one row's slot
-  long long T_;
-  __device__ __forceinline__ T* at(int s, int j, int o) const {
-    return reinterpret_cast<T*>(base + ((s * OPS + o) * ROWS + j) * slot);
-  }
-  // the rows from r0 into stage s; false when there are none
-  __device__ __forceinline__ bool fill(int s, long long r0, const T* const (&m)[OPS], const long long (&ld)[OPS]) const {
-    if (r0 >= T_) return false;
-    const int rows = T_ - r0 < ROWS ? static_cast<int>(T_ - r0) : ROWS;
-    uint32_t bytes = 0;
-    if (V > 1) {
-      bytes = static_cast<uint32_t>(rows * OPS * C) * sizeof(T);
-    } else {
-#pragma unroll
-      for (int j = 0; j < ROWS; ++j)
-        if (j < rows)
-#pragma unroll
-          for (int o = 0; o < OPS; ++o) {
-            const RowSpan<T, V> q(m[o] + (r0 + j) * ld[o], C);
-            bytes += static_cast<uint32_t>(q.hi - q.lo) * sizeof(T);
-          }
-    }
-    mbar_arrive_expect_tx(&full[s], bytes);
-#pragma unroll
-    for (int o = 0; o < OPS; ++o) {
-      if (V > 1 && ld[o] == C) {           // whole rows one after another: one copy
-        bulk_load(at(s, 0, o), m[o] + r0 * ld[o], static_cast<uint32_t>(rows * C) * sizeof(T), &full[s]);
-        continue;
-      }
-#pragma unroll
-      for (int j = 0; j < ROWS; ++j)
-        if (j < rows) {
-          const RowSpan<T, V> q(m[o] + (r0 + j) * ld[o], C);
-          if (q.hi > q.lo)
-            bulk_load(at(s, j, o) + q.off + q.lo, q.row + q.lo, static_cast<uint32_t>(q.hi - q.lo) * sizeof(T), &full[s]);
-        }
-    }
-    return true;
-  }
-};
-
-// A CTA's walk over its turns: rows, stage and the stage's phase.
-template <int ROWS>
-struct Turn {
-  long long row, step;                   // the turn's first row; rows between turns
+  uint32_t base;                         // shared-memory address of this turn's stage
   int s;
   uint32_t phase;
-  __device__ __forceinline__ Turn() : row(static_cast<long long>(blockIdx.x) * ROWS),
-                                      step(static_cast<long long>(gridDim.x) * ROWS), s(0), phase(0) {}
-  __device__ __forceinline__ void next(int stages) {
-    row += step;
-    if (++s == stages) {
+  int row, step;                         // this turn's first row; rows between turns
+
+  __device__ __forceinline__ Walk(const NormParams& p_, void* mem, uint64_t* full_)
+      : p(p_), full(full_), base(smem_u32(mem)), s(0), phase(0), row(static_cast<int>(blockIdx.x) * ROWS),
+        step(static_cast<int>(gridDim.x) * ROWS) {}
+  __device__ __forceinline__ int total() const { return static_cast<int>(p.T); }
+  __device__ __forceinline__ uint32_t stage_bytes() const { return static_cast<uint32_t>(p.slot) * (ROWS * OPS); }
+  __device__ __forceinline__ bool more() const { return row < total(); }
+  __device__ __forceinline__ void next() {
+    row = total() - row > step ? row + step : total();
+    base += stage_bytes();
+    if (++s == p.stages) {
       s = 0;
       phase ^= 1;
+      base -= static_cast<uint32_t>(p.stages) * stage_bytes();
+    }
+  }
+  // shared-memory address of row j of operand o in this turn's stage
+  __device__ __forceinline__ uint32_t at(int j, int o) const {
+    return base + static_cast<uint32_t>((o * ROWS + j) * p.slot);
+  }
+  __device__ __forceinline__ const T* src(int o, long long r) const {
+    return o == 0 ? static_cast<const T*>(p.x) + r * p.ldx : static_cast<const T*>(p.dy) + r * p.lddy;
+  }
+  // the rows from r0 (64-bit: it may lie past the end) into the stage at `dst` (thread 0)
+  __device__ __forceinline__ void fill(uint32_t dst, int stage, long long r0) const {
+    if (r0 >= p.T) return;
+    const int n = p.T - r0 < ROWS ? static_cast<int>(p.T - r0) : ROWS;
+    uint64_t* bar = &full[stage];
+    uint32_t bytes = 0;
+    if (V > 1) {
+      bytes = static_cast<uint32_t>(n * OPS * p.C) * sizeof(T);
+    } else {
+      for (int o = 0; o < OPS; ++o)
+        for (int j = 0; j < n; ++j) {
+          const RowSpan<T, V> q(src(o, r0 + j), p.C);
+          bytes += static_cast<uint32_t>(q.hi - q.lo) * sizeof(T);
+        }
+    }
+    mbar_arrive_expect_tx(bar, bytes);
+    for (int o = 0; o < OPS; ++o) {
+      const uint32_t d = dst + static_cast<uint32_t>(o * ROWS * p.slot);
+      if (V > 1 && (o == 0 ? p.ldx : p.lddy) == p.C) {   // whole rows one after another: one copy
+        bulk_load(d, src(o, r0), static_cast<uint32_t>(n * p.C) * sizeof(T), bar);
+        continue;
+      }
+      for (int j = 0; j < n; ++j) {
+        const RowSpan<T, V> q(src(o, r0 + j), p.C);
+        if (q.hi > q.lo)
+          bulk_load(d + j * p.slot + (q.off + q.lo) * static_cast<int>(sizeof(T)), q.row + q.lo,
+                    static_cast<uint32_t>(q.hi - q.lo) * sizeof(T), bar);
+      }
+    }
+  }
+  __device__ __forceinline__ void refill() const {       // this turn's stage, `stages` turns on
+    if (threadIdx.x == 0) fill(base, s, row + static_cast<long long>(step) * p.stages);
+  }
+  // Barriers, then the first `stages` turns on their way.
+  __device__ __forceinline__ void begin(volatile int* abort_flag) const {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < p.stages; ++i) mbar_init(&full[i], 1);
+      *abort_flag = 0;
+      fence_barrier_init();
+      fence_proxy_async_smem();
+      for (int i = 0; i < p.stages; ++i) fill(base + i * stage_bytes(), i, row + static_cast<long long>(step) * i);
+    }
+    __syncthreads();
+  }
+  // The last turn may hold fewer than ROWS rows: the missing ones read as zeros, so that the turn
+  // needs no tests (a CTA barrier in that turn only).
+  __device__ __forceinline__ void pad() const {
+    const int n = total() - row;
+    if (n >= ROWS) return;
+    for (int o = 0; o < OPS; ++o)
+      for (uint32_t b = threadIdx.x * 4; b < static_cast<uint32_t>((ROWS - n) * p.slot); b += blockDim.x * 4)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at(n, o) + b), "r"(0) : "memory");
+    __syncthreads();
+  }
+  // After an expired wait: the copies still in flight land before the CTA leaves (this turn's and
+  // those of the stages - 1 turns after it).
+  __device__ __forceinline__ void settle() {
+    if (threadIdx.x != 0) return;
+    for (int k = 0; k < p.stages && more(); ++k, next()) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&full[s]), phase) && globaltimer_ns() - t0 < 100000000ull) {
+      }
     }
   }
 };
 
 // One element of a row in its slot (or, outside the slot's span, in global memory)
 template <typename T>
-__device__ __forceinline__ float slot_at(const T* slot, const RowSpan<T, 1>& q, int c) {
+__device__ __forceinline__ float slot_at(uint32_t slot, const RowSpan<T, 1>& q, int c) {
   if (c < q.lo || c >= q.hi) {
     Raw<T, 1> r;
     r.load(q.row + c);
     return r.at(0);
   }
-  if constexpr (sizeof(T) == 2) return __uint_as_float(static_cast<uint32_t>(slot[q.off + c]) << 16);
-  else return slot[q.off + c];
+  const uint32_t a = slot + static_cast<uint32_t>(q.off + c) * static_cast<uint32_t>(sizeof(T));
+  if constexpr (sizeof(T) == 2) {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a));
+    return __uint_as_float(static_cast<uint32_t>(h) << 16);
+  } else {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a));
+    return f;
+  }
 }
 
 // Chunk i of a row, as loaded (V > 1: the raw vector; V = 1: two floats), and its values.  The
@@ -327,11 +357,11 @@ template <typename T, int V>
 struct RawChunk {
   static constexpr int kWords = V > 1 ? 4 : 2;
   uint32_t u[kWords];
-  __device__ __forceinline__ void load(const T* slot, const RowSpan<T, V>& q, int c, int C) {
+  __device__ __forceinline__ void load(uint32_t slot, const RowSpan<T, V>& q, int c, int C) {
     if constexpr (V > 1) {
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                   : "r"(smem_u32(slot) + static_cast<uint32_t>(c) * static_cast<uint32_t>(sizeof(T))));
+                   : "r"(slot + static_cast<uint32_t>(c) * static_cast<uint32_t>(sizeof(T))));
     } else {
       const int c1 = c + static_cast<int>(blockDim.x);
       u[0] = __float_as_uint(slot_at(slot, q, c));
@@ -397,33 +427,6 @@ __device__ __forceinline__ void store_sums(float* row, const Chunk<V>& x, int c,
   }
 }
 
-// Set up the ring: barriers, then the first `stages` turns on their way.
-template <typename T, int V, int ROWS, int OPS>
-__device__ __forceinline__ void ring_begin(RowRing<T, V, ROWS, OPS>& ring, const T* const (&m)[OPS],
-                                           const long long (&ld)[OPS], volatile int* abort_flag) {
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < ring.stages; ++s) mbar_init(&ring.full[s], 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-    fence_proxy_async_smem();
-    Turn<ROWS> t;
-    for (int s = 0; s < ring.stages; ++s, t.next(ring.stages)) ring.fill(s, t.row, m, ld);
-  }
-  __syncthreads();
-}
-
-// After an expired wait: the copies still in flight land before the CTA leaves (this turn's and
-// those of the stages - 1 turns after it).
-template <typename T, int V, int ROWS, int OPS>
-__device__ __forceinline__ void ring_settle(const RowRing<T, V, ROWS, OPS>& ring, Turn<ROWS> t) {
-  if (threadIdx.x != 0) return;
-  for (int k = 0; k < ring.stages && t.row < ring.T_; ++k, t.next(ring.stages)) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(smem_u32(&ring.full[t.s]), t.phase) && globaltimer_ns() - t0 < 100000000ull) {
-    }
-  }
-}
-
 // The chunks of a weight or bias vector that a thread's columns need; kHold: kept in registers for
 // all rows, else loaded again at each use (where they would not fit beside the row).
 template <int V, int NC, bool kHold>
@@ -431,69 +434,76 @@ struct Held {
   Chunk<V> c[kHold ? NC : 1];
   const void* p;
   int f32, vec, C;
-  __device__ __forceinline__ Held(const void* p_, int f32_, int vec_, int C_) : p(p_), f32(f32_), vec(vec_), C(C_) {
-    if (kHold && p)
+  float none;                            // what a missing vector stands for (1 or 0)
+  __device__ __forceinline__ Held(const void* p_, int f32_, int vec_, int C_, float none_)
+      : p(p_), f32(f32_), vec(vec_), C(C_), none(none_) {
+    if (kHold)
 #pragma unroll
-      for (int i = 0; i < (kHold ? NC : 1); ++i) {
-        c[i].zero();
-        if (chunk_col<V>(i) < C) c[i] = vec_chunk<V>(p, f32, vec, chunk_col<V>(i), C);
-      }
+      for (int i = 0; i < (kHold ? NC : 1); ++i) c[i] = load(i);
   }
-  __device__ __forceinline__ Chunk<V> at(int i) const {
-    return kHold ? c[kHold ? i : 0] : vec_chunk<V>(p, f32, vec, chunk_col<V>(i), C);
+  __device__ __forceinline__ Chunk<V> load(int i) const {
+    Chunk<V> o;
+    if (p && chunk_col<V>(i) < C) return vec_chunk<V>(p, f32, vec, chunk_col<V>(i), C);
+#pragma unroll
+    for (int k = 0; k < Chunk<V>::kPairs; ++k) o.p[k] = f2(none, none);
+    return o;
   }
+  __device__ __forceinline__ Chunk<V> at(int i) const { return kHold ? c[kHold ? i : 0] : load(i); }
 };
 
-// Forward, ROWS rows of a CTA per turn (a CTA is one warp where that is enough); NC chunks a thread.
-template <typename T, int V, int NC, int ROWS, bool kHold>
-__global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams p, const bool layer) {
+// The span of row j of a turn (V = 1): a padded row lies wholly in its slot.
+template <typename T, int V, int ROWS, int OPS>
+__device__ __forceinline__ RowSpan<T, V> span_of(const Walk<T, V, ROWS, OPS>& walk, int o, int j) {
+  RowSpan<T, V> q(V > 1 ? nullptr : walk.src(o, min(walk.row + j, walk.total() - 1)), walk.p.C);
+  if (V == 1 && walk.row + j >= walk.total()) {
+    q.off = q.lo = 0;
+    q.hi = walk.p.C;
+  }
+  return q;
+}
+
+// Forward, ROWS rows of a CTA per turn (a CTA is one warp where that is enough); NC chunks a thread,
+// all of which exist in every thread when kExact.
+template <typename T, int V, int NC, int ROWS, bool kHold, int kRegs, bool kExact>
+__global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_fwd_kernel(const NormParams p, const bool layer) {
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[2][16 * ROWS];
   __shared__ uint64_t full[kMaxStages];
   __shared__ int abort_word;
   constexpr int P = Chunk<V>::kPairs;
-  const T* const m[1] = {static_cast<const T*>(p.x)};
-  const long long ld[1] = {p.ldx};
-  RowRing<T, V, ROWS, 1> ring{ring_mem, full, p.stages, p.slot, p.C, p.T};
-  ring_begin(ring, m, ld, &abort_word);
-  const Held<V, NC, kHold> w(p.w, p.w_f32, p.w_vec, p.C), b(p.b, p.b_f32, p.b_vec, p.C);
+  Walk<T, V, ROWS, 1> walk(p, ring_mem, full);
+  walk.begin(&abort_word);
+  const Held<V, NC, kHold> w(p.w, p.w_f32, p.w_vec, p.C, 1.f), b(p.b, p.b_f32, p.b_vec, p.C, 0.f);
+  auto have = [&](int i) { return kExact || chunk_col<V>(i) < p.C; };
+  T* y = static_cast<T*>(p.y) + walk.row * p.ldy;
+  const long long y_step = walk.step * p.ldy;
   bool fail = false;
-  Turn<ROWS> turn;
   int odd = 0;
-  for (; turn.row < p.T; turn.next(p.stages)) {
-    const int rows = p.T - turn.row < ROWS ? static_cast<int>(p.T - turn.row) : ROWS;
-    fail = !mbar_wait(&full[turn.s], turn.phase, &abort_word, p.timeout_ns, p.status);
+  for (; walk.more(); walk.next(), y += y_step) {
+    fail = !mbar_wait(&full[walk.s], walk.phase, &abort_word, p.timeout_ns, p.status);
+    walk.pad();
     Chunk<V> x[ROWS][NC];
     float sum[ROWS], mu[ROWS];
-    F2 t[ROWS];
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      t[j] = f2(0.f, 0.f);
+      const RowSpan<T, V> q = span_of(walk, 0, j);
+      F2 t = f2(0.f, 0.f);
       mu[j] = 0.f;
-      const RowSpan<T, V> q(m[0] + (turn.row + j) * p.ldx, p.C);
-      const T* slot = ring.at(turn.s, j, 0);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int c = chunk_col<V>(i);
-        if (c < p.C && j < rows) {
+        if (have(i)) {
           RawChunk<T, V> r;
-          r.load(slot, q, c, p.C);
+          r.load(walk.at(j, 0), q, chunk_col<V>(i), p.C);
           x[j][i] = r.values();
         } else {
           x[j][i].zero();
         }
+#pragma unroll
+        for (int k = 0; k < P; ++k) t = f2_add(t, x[j][i].p[k]);
       }
+      sum[j] = f2_sum(t);
     }
     if (layer) {
-#pragma unroll
-      for (int j = 0; j < ROWS; ++j) {
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-#pragma unroll
-          for (int k = 0; k < P; ++k) t[j] = f2_add(t[j], x[j][i].p[k]);
-        sum[j] = f2_sum(t[j]);
-        t[j] = f2(0.f, 0.f);
-      }
       cta_sum<ROWS>(sum, red[odd], fail);
       odd ^= 1;
 #pragma unroll
@@ -501,58 +511,50 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams 
         mu[j] = sum[j] * p.inv_c;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-          const int c = chunk_col<V>(i);
-          if (c < p.C) {
-            const F2 nm = f2(-mu[j], V == 1 && c + static_cast<int>(blockDim.x) >= p.C ? 0.f : -mu[j]);
+          const F2 nm = f2(have(i) ? -mu[j] : 0.f,
+                           !have(i) || (V == 1 && chunk_col<V>(i) + static_cast<int>(blockDim.x) >= p.C) ? 0.f : -mu[j]);
 #pragma unroll
-            for (int k = 0; k < P; ++k) x[j][i].p[k] = f2_add(x[j][i].p[k], nm);
-          }
+          for (int k = 0; k < P; ++k) x[j][i].p[k] = f2_add(x[j][i].p[k], nm);
         }
       }
     }
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
+      F2 t = f2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int k = 0; k < P; ++k) t[j] = f2_fma(x[j][i].p[k], x[j][i].p[k], t[j]);
-      sum[j] = f2_sum(t[j]);
+        for (int k = 0; k < P; ++k) t = f2_fma(x[j][i].p[k], x[j][i].p[k], t);
+      sum[j] = f2_sum(t);
     }
     cta_sum<ROWS>(sum, red[odd], fail);  // every thread has read the stage; `fail` is now the CTA's
     odd ^= 1;
-    if (threadIdx.x == 0 && !fail) ring.fill(turn.s, turn.row + turn.step * p.stages, m, ld);
+    if (!fail) walk.refill();
+    const int rows = walk.total() - walk.row;
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      sum[j] = 1.0f / sqrtf(sum[j] * p.inv_c + p.eps);
+      sum[j] = rsqrtf(sum[j] * p.inv_c + p.eps);   // within 2 ulp, a twentieth of a root and a quotient
       if (p.stats && threadIdx.x == 0 && j < rows) {
-        p.stats[turn.row + j] = mu[j];
-        p.stats[p.T + turn.row + j] = sum[j];
+        p.stats[walk.row + j] = mu[j];
+        p.stats[p.T + walk.row + j] = sum[j];
       }
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = chunk_col<V>(i);
-      if (c < p.C) {
-        Chunk<V> wc, bc;
-        if (p.w) wc = w.at(i);
-        if (p.b) bc = b.at(i);
+      if (have(i)) {
+        const Chunk<V> wc = w.at(i), bc = b.at(i);
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-          if (j >= rows) continue;
           const F2 rr = f2(sum[j], sum[j]);
 #pragma unroll
-          for (int k = 0; k < P; ++k) {
-            x[j][i].p[k] = f2_mul(x[j][i].p[k], rr);
-            if (p.w) x[j][i].p[k] = f2_mul(x[j][i].p[k], wc.p[k]);
-            if (p.b) x[j][i].p[k] = f2_add(x[j][i].p[k], bc.p[k]);
-          }
-          store_chunk<T, V>(static_cast<T*>(p.y) + (turn.row + j) * p.ldy, x[j][i], c, p.C);
+          for (int k = 0; k < P; ++k) x[j][i].p[k] = f2_fma(f2_mul(x[j][i].p[k], rr), wc.p[k], bc.p[k]);
+          if (j < rows) store_chunk<T, V>(y + j * p.ldy, x[j][i], chunk_col<V>(i), p.C);
         }
       }
     }
     if (fail) break;
   }
-  if (fail) ring_settle(ring, turn);
+  if (fail) walk.settle();
 }
 
 // Rows too long for the registers of 512 threads: three passes over the row.
@@ -605,139 +607,127 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_long_kernel(const NormPa
 // Backward, ROWS rows of a CTA per turn; NC chunks a thread.  Between the sums and dx a thread keeps
 // xh and h of its columns, or (kRaw, where those and dw, db would not fit its registers) the raw
 // elements, and forms them again.
-template <typename T, int V, int NC, int ROWS, bool kRaw, bool kHold>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams p, const bool layer) {
+template <typename T, int V, int NC, int ROWS, bool kRaw, bool kHold, int kRegs, bool kExact>
+__global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kernel(const NormParams p, const bool layer) {
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[2][16 * 2 * ROWS];
   __shared__ uint64_t full[kMaxStages];
   __shared__ int abort_word;
   constexpr int P = Chunk<V>::kPairs;
-  const T* const m[2] = {static_cast<const T*>(p.x), static_cast<const T*>(p.dy)};
-  const long long ld[2] = {p.ldx, p.lddy};
-  RowRing<T, V, ROWS, 2> ring{ring_mem, full, p.stages, p.slot, p.C, p.T};
-  ring_begin(ring, m, ld, &abort_word);
+  Walk<T, V, ROWS, 2> walk(p, ring_mem, full);
+  walk.begin(&abort_word);
+  auto have = [&](int i) { return kExact || chunk_col<V>(i) < p.C; };
+  const Held<V, NC, kHold> wh(p.w, p.w_f32, p.w_vec, p.C, 1.f);
   Chunk<V> dw[NC], db[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     dw[i].zero();
     db[i].zero();
   }
-  const Held<V, NC, kHold> wh(p.w, p.w_f32, p.w_vec, p.C);
+  T* y = static_cast<T*>(p.y) + (p.y ? walk.row * p.ldy : 0);
+  const long long y_step = walk.step * p.ldy;
   bool fail = false;
-  Turn<ROWS> turn;
   int odd = 0;
-  // the rows' mu and r, read a turn ahead
+  // the rows' mu and r, read a turn ahead; a padded row's r is zero, so that it adds nothing
   float mu_n[ROWS], r_n[ROWS];
-  auto stats_of = [&](long long row0) {
+  auto stats_of = [&](int row0) {
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      const bool ok = row0 + j < p.T;
-      mu_n[j] = layer && ok ? __ldg(p.stats + row0 + j) : 0.f;
-      r_n[j] = ok ? __ldg(p.stats + p.T + row0 + j) : 0.f;
+      const int t = min(row0 + j, walk.total() - 1);
+      mu_n[j] = layer ? __ldg(p.stats + t) : 0.f;
+      r_n[j] = __ldg(p.stats + p.T + t);
+      if (row0 + j >= walk.total()) mu_n[j] = r_n[j] = 0.f;
     }
   };
-  stats_of(turn.row);
-  for (; turn.row < p.T; turn.next(p.stages), odd ^= 1) {
-    const long long row0 = turn.row;
-    const int s = turn.s;
-    const int rows = p.T - row0 < ROWS ? static_cast<int>(p.T - row0) : ROWS;
-    F2 nm[ROWS], rr[ROWS], s1[ROWS], s2[ROWS];
+  stats_of(walk.row);
+  for (; walk.more(); walk.next(), odd ^= 1, y += y_step) {
+    float mu[ROWS], r[ROWS];
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      nm[j] = f2(-mu_n[j], -mu_n[j]);
-      rr[j] = f2(r_n[j], r_n[j]);
-      s1[j] = s2[j] = f2(0.f, 0.f);
+      mu[j] = mu_n[j];
+      r[j] = r_n[j];
     }
-    stats_of(row0 + turn.step);
-    fail = !mbar_wait(&full[s], turn.phase, &abort_word, p.timeout_ns, p.status);
+    if (walk.total() - walk.row > walk.step) stats_of(walk.row + walk.step);
+    fail = !mbar_wait(&full[walk.s], walk.phase, &abort_word, p.timeout_ns, p.status);
+    walk.pad();
     Chunk<V> x[ROWS][kRaw ? 1 : NC], h[ROWS][kRaw ? 1 : NC];     // xh and dy w
     RawChunk<T, V> rx[ROWS][kRaw ? NC : 1], rg[ROWS][kRaw ? NC : 1];
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int c = chunk_col<V>(i);
-      if (c < p.C) {
-        Chunk<V> w;
-        if (p.w) w = wh.at(i);
-#pragma unroll
-        for (int j = 0; j < ROWS; ++j) {
-          if (j >= rows) continue;
-          RawChunk<T, V> a, g;
-          a.load(ring.at(s, j, 0), RowSpan<T, V>(m[0] + (row0 + j) * ld[0], p.C), c, p.C);
-          g.load(ring.at(s, j, 1), RowSpan<T, V>(m[1] + (row0 + j) * ld[1], p.C), c, p.C);
-          if (kRaw) {
-            rx[j][i] = a;
-            rg[j][i] = g;
-          }
-          Chunk<V> xh = a.values(), hh = g.values();
-#pragma unroll
-          for (int k = 0; k < P; ++k) {
-            xh.p[k] = f2_mul(f2_add(xh.p[k], nm[j]), rr[j]);
-            dw[i].p[k] = f2_fma(hh.p[k], xh.p[k], dw[i].p[k]);
-            db[i].p[k] = f2_add(db[i].p[k], hh.p[k]);
-            if (p.w) hh.p[k] = f2_mul(hh.p[k], w.p[k]);
-            s1[j] = f2_add(s1[j], hh.p[k]);
-            s2[j] = f2_fma(hh.p[k], xh.p[k], s2[j]);
-          }
-          if (!kRaw) {
-            x[j][i] = xh;
-            h[j][i] = hh;
-          }
-        }
-      }
-    }
     float sums[2 * ROWS];
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      sums[2 * j] = f2_sum(s1[j]);
-      sums[2 * j + 1] = f2_sum(s2[j]);
+      const RowSpan<T, V> qx = span_of(walk, 0, j), qg = span_of(walk, 1, j);
+      const F2 nm = f2(-mu[j], -mu[j]), rr = f2(r[j], r[j]);
+      F2 s1 = f2(0.f, 0.f), s2 = f2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        if (!have(i)) continue;
+        const Chunk<V> w = wh.at(i);
+        RawChunk<T, V> a, g;
+        a.load(walk.at(j, 0), qx, chunk_col<V>(i), p.C);
+        g.load(walk.at(j, 1), qg, chunk_col<V>(i), p.C);
+        if (kRaw) {
+          rx[j][kRaw ? i : 0] = a;
+          rg[j][kRaw ? i : 0] = g;
+        }
+        Chunk<V> xh = a.values(), hh = g.values();
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          xh.p[k] = f2_mul(f2_add(xh.p[k], nm), rr);
+          dw[i].p[k] = f2_fma(hh.p[k], xh.p[k], dw[i].p[k]);
+          db[i].p[k] = f2_add(db[i].p[k], hh.p[k]);
+          hh.p[k] = f2_mul(hh.p[k], w.p[k]);
+          s1 = f2_add(s1, hh.p[k]);
+          s2 = f2_fma(hh.p[k], xh.p[k], s2);
+        }
+        if (!kRaw) {
+          x[j][kRaw ? 0 : i] = xh;
+          h[j][kRaw ? 0 : i] = hh;
+        }
+      }
+      sums[2 * j] = f2_sum(s1);
+      sums[2 * j + 1] = f2_sum(s2);
     }
     cta_sum<2 * ROWS>(sums, red[odd], fail);   // every thread has read the stage; `fail` is the CTA's
-    if (threadIdx.x == 0 && !fail) ring.fill(turn.s, turn.row + turn.step * p.stages, m, ld);
+    if (!fail) walk.refill();
     if (p.y) {
+      const int rows = walk.total() - walk.row;
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
-        if (j >= rows) continue;
         const float m1 = layer ? sums[2 * j] * p.inv_c : 0.f, m2 = sums[2 * j + 1] * p.inv_c;
-        const F2 a = f2(-m1, -m1), b = f2(-m2, -m2);
-        T* yr = static_cast<T*>(p.y) + (row0 + j) * p.ldy;
+        const F2 a = f2(-m1, -m1), b = f2(-m2, -m2), rr = f2(r[j], r[j]), nm = f2(-mu[j], -mu[j]);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-          const int c = chunk_col<V>(i);
-          if (c < p.C) {
-            Chunk<V> xh, hh;
-            if (kRaw) {
-              xh = rx[j][i].values();
-              hh = rg[j][i].values();
-              Chunk<V> w;
-              if (p.w) w = wh.at(i);
+          if (!have(i)) continue;
+          Chunk<V> xh, hh;
+          if (kRaw) {
+            xh = rx[j][kRaw ? i : 0].values();
+            hh = rg[j][kRaw ? i : 0].values();
+            const Chunk<V> w = wh.at(i);
 #pragma unroll
-              for (int k = 0; k < P; ++k) {
-                xh.p[k] = f2_mul(f2_add(xh.p[k], nm[j]), rr[j]);
-                if (p.w) hh.p[k] = f2_mul(hh.p[k], w.p[k]);
-              }
-            } else {
-              xh = x[j][i];
-              hh = h[j][i];
+            for (int k = 0; k < P; ++k) {
+              xh.p[k] = f2_mul(f2_add(xh.p[k], nm), rr);
+              hh.p[k] = f2_mul(hh.p[k], w.p[k]);
             }
-#pragma unroll
-            for (int k = 0; k < P; ++k) xh.p[k] = f2_mul(f2_fma(xh.p[k], b, f2_add(hh.p[k], a)), rr[j]);
-            store_chunk<T, V>(yr, xh, c, p.C);
+          } else {
+            xh = x[j][kRaw ? 0 : i];
+            hh = h[j][kRaw ? 0 : i];
           }
+#pragma unroll
+          for (int k = 0; k < P; ++k) xh.p[k] = f2_mul(f2_fma(xh.p[k], b, f2_add(hh.p[k], a)), rr);
+          if (j < rows) store_chunk<T, V>(y + j * p.ldy, xh, chunk_col<V>(i), p.C);
         }
       }
     }
     if (fail) break;
   }
-  if (fail) ring_settle(ring, turn);
+  if (fail) walk.settle();
   if (!p.part) return;
   float* out = p.part + static_cast<long long>(blockIdx.x) * 2 * p.C;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int c = chunk_col<V>(i);
-    if (c < p.C) {
-      store_sums<V>(out, dw[i], c, p.C);
-      store_sums<V>(out + p.C, db[i], c, p.C);
-    }
+    if (!have(i)) continue;
+    store_sums<V>(out, dw[i], chunk_col<V>(i), p.C);
+    store_sums<V>(out + p.C, db[i], chunk_col<V>(i), p.C);
   }
 }
 
@@ -823,10 +813,10 @@ bool valid_vec(const wp_mat* v, long long C) {
          v->rows * v->cols == C;
 }
 
-// How a row length is worked on: vectors (or single elements) per thread (0: the long form), rows per turn, threads,
-// CTAs per SM, ring stages and bytes of a row's slot.
+// How a row length is worked on: vectors (or single elements) per thread (0: the long form), rows
+// per turn, threads, registers a thread, CTAs per SM, ring stages and bytes of a row's slot.
 struct Form {
-  int nv, rows, threads, per_sm, stages, slot;
+  int nv, rows, threads, regs, per_sm, stages, slot;
 };
 
 // Threads that share a row: each holds nv vectors of it, a whole number of warps in all.
@@ -834,13 +824,13 @@ int row_threads(long long vectors, int nv) {
   return static_cast<int>(((vectors + nv - 1) / nv + 31) / 32 * 32);
 }
 
-// The ring of a form: as many CTAs per SM as 128 registers a thread allow (at most 16), the
+// The ring of a form: as many CTAs per SM as its registers allow (at most 16), the
 // stages that then fit their shared memory, at most kMaxStages; fewer CTAs when two stages do not.
 bool ring_form(Form* f, long long C, bool f32, bool vec, int ops) {
   const int size = f32 ? 4 : 2;
   f->slot = static_cast<int>((C * size + 15) / 16 * 16 + (vec ? 0 : 16));
   const size_t stage = static_cast<size_t>(f->rows) * ops * f->slot;
-  f->per_sm = kMaxThreads / f->threads;
+  f->per_sm = 65536 / (f->threads * f->regs);
   if (f->per_sm > 16) f->per_sm = 16;
   if (f->per_sm < 1) f->per_sm = 1;
   for (;; --f->per_sm) {
@@ -855,40 +845,42 @@ bool ring_form(Form* f, long long C, bool f32, bool vec, int ops) {
 // elements (waits, sums, barriers) is spread over 64; longer rows take more elements and fewer rows.
 Form fwd_form(long long C, bool f32, bool vec) {
   const long long n = vec ? C / (f32 ? 4 : 8) : C;
-  Form f{0, 1, kMaxThreads, 2, 0, 0};
+  Form f{0, 1, kMaxThreads, 64, 2, 0, 0};
   if (C > (1 << 20)) return f;
-  struct { int nv, rows, top; } const vecs[] = {{1, 4, 64}, {2, 4, 512}, {4, 2, 512}, {8, 1, 512}},
-                                      ones[] = {{2, 4, 64}, {8, 4, 384}, {16, 2, 512}, {32, 1, 512}};
+  struct { int nv, rows, top, regs; } const vecs[] = {{1, 4, 64, 104}, {2, 4, 512, 112}, {4, 2, 512, 112}, {8, 1, 512, 128}},
+                                            ones[] = {{2, 4, 64, 64}, {8, 4, 384, 96}, {16, 2, 512, 112}, {32, 1, 512, 96}};
   for (int i = 0; i < 4; ++i) {
     const auto& q = vec ? vecs[i] : ones[i];
     if (n <= static_cast<long long>(q.nv) * q.top) {
       f.nv = q.nv;
       f.rows = q.rows;
+      f.regs = q.regs;
       f.threads = row_threads(n, q.nv);
       break;
     }
   }
-  if (f.nv && !ring_form(&f, C, f32, vec, 1)) f = Form{0, 1, kMaxThreads, 2, 0, 0};
+  if (f.nv && !ring_form(&f, C, f32, vec, 1)) f = Form{0, 1, kMaxThreads, 64, 2, 0, 0};
   return f;
 }
 
 // Backward: fewer elements a thread (its dw, db, weight, xh and h take registers each).
 Form bwd_form(long long C, bool f32, bool vec) {
   const long long n = vec ? C / (f32 ? 4 : 8) : C;
-  Form f{0, 1, kMaxThreads, 2, 0, 0};
+  Form f{0, 1, kMaxThreads, 64, 2, 0, 0};
   if (C > (1 << 20)) return f;
-  struct { int nv, rows, top; } const vecs[] = {{1, 4, 384}, {2, 1, 384}, {4, 1, 512}, {4, 1, 512}},
-                                      ones[] = {{2, 4, 256}, {8, 2, 288}, {16, 1, 512}, {28, 1, 512}};
+  struct { int nv, rows, top, regs; } const vecs[] = {{1, 4, 384, 128}, {2, 1, 384, 128}, {4, 1, 512, 128}, {4, 1, 512, 128}},
+                                            ones[] = {{2, 4, 256, 112}, {8, 2, 288, 112}, {16, 1, 512, 128}, {28, 1, 512, 128}};
   for (int i = 0; i < 4; ++i) {
     const auto& q = vec ? vecs[i] : ones[i];
     if (n <= static_cast<long long>(q.nv) * q.top) {
       f.nv = q.nv;
       f.rows = q.rows;
+      f.regs = q.regs;
       f.threads = row_threads(n, q.nv);
       break;
     }
   }
-  if (f.nv && !ring_form(&f, C, f32, vec, 2)) f = Form{0, 1, kMaxThreads, 2, 0, 0};
+  if (f.nv && !ring_form(&f, C, f32, vec, 2)) f = Form{0, 1, kMaxThreads, 64, 2, 0, 0};
   return f;
 }
 
@@ -923,19 +915,24 @@ int dispatch_fwd(NormParams p, bool vec, bool layer, cudaStream_t st) {
   p.slot = f.slot;
   const size_t smem = static_cast<size_t>(f.stages) * f.rows * f.slot;
   const int g = blocks_of(p.T, f);
+  const bool exact = vec && p.C == f.nv * f.threads * V;
+#define WP_FWD(...) \
+  (exact ? launch(norm_fwd_kernel<T, V, __VA_ARGS__, true>, g, f, smem, p, layer, st) \
+         : launch(norm_fwd_kernel<T, V, __VA_ARGS__, false>, g, f, smem, p, layer, st))
   if (vec) {
     switch (f.nv) {
-      case 1: return launch(norm_fwd_kernel<T, V, 1, 4, true>, g, f, smem, p, layer, st);
-      case 2: return launch(norm_fwd_kernel<T, V, 2, 4, sizeof(T) == 4>, g, f, smem, p, layer, st);
-      case 4: return launch(norm_fwd_kernel<T, V, 4, 2, false>, g, f, smem, p, layer, st);
-      default: return launch(norm_fwd_kernel<T, V, 8, 1, false>, g, f, smem, p, layer, st);
+      case 1: return WP_FWD(1, 4, true, 104);
+      case 2: return WP_FWD(2, 4, false, 112);
+      case 4: return WP_FWD(4, 2, false, 112);
+      default: return WP_FWD(8, 1, false, 128);
     }
   }
+#undef WP_FWD
   switch (f.nv) {                        // two elements a chunk
-    case 2: return launch(norm_fwd_kernel<T, 1, 1, 4, true>, g, f, smem, p, layer, st);
-    case 8: return launch(norm_fwd_kernel<T, 1, 4, 4, true>, g, f, smem, p, layer, st);
-    case 16: return launch(norm_fwd_kernel<T, 1, 8, 2, true>, g, f, smem, p, layer, st);
-    default: return launch(norm_fwd_kernel<T, 1, 16, 1, false>, g, f, smem, p, layer, st);
+    case 2: return launch(norm_fwd_kernel<T, 1, 1, 4, true, 64, false>, g, f, smem, p, layer, st);
+    case 8: return launch(norm_fwd_kernel<T, 1, 4, 4, true, 96, false>, g, f, smem, p, layer, st);
+    case 16: return launch(norm_fwd_kernel<T, 1, 8, 2, true, 112, false>, g, f, smem, p, layer, st);
+    default: return launch(norm_fwd_kernel<T, 1, 16, 1, false, 96, false>, g, f, smem, p, layer, st);
   }
 }
 
@@ -951,18 +948,23 @@ int dispatch_bwd(NormParams p, bool vec, bool layer, int* grid, cudaStream_t st)
   p.stages = f.stages;
   p.slot = f.slot;
   const size_t smem = static_cast<size_t>(f.stages) * f.rows * 2 * f.slot;
+  const bool exact = vec && p.C == f.nv * f.threads * V;
+#define WP_BWD(...) \
+  (exact ? launch(norm_bwd_kernel<T, V, __VA_ARGS__, true>, g, f, smem, p, layer, st) \
+         : launch(norm_bwd_kernel<T, V, __VA_ARGS__, false>, g, f, smem, p, layer, st))
   if (vec) {
     switch (f.nv) {
-      case 1: return launch(norm_bwd_kernel<T, V, 1, 4, false, true>, g, f, smem, p, layer, st);
-      case 2: return launch(norm_bwd_kernel<T, V, 2, 1, false, true>, g, f, smem, p, layer, st);
-      default: return launch(norm_bwd_kernel<T, V, 4, 1, sizeof(T) == 2, false>, g, f, smem, p, layer, st);
+      case 1: return WP_BWD(1, 4, false, true, 128);
+      case 2: return WP_BWD(2, 1, false, true, 128);
+      default: return WP_BWD(4, 1, sizeof(T) == 2, false, 128);
     }
   }
+#undef WP_BWD
   switch (f.nv) {                        // two elements a chunk
-    case 2: return launch(norm_bwd_kernel<T, 1, 1, 4, false, true>, g, f, smem, p, layer, st);
-    case 8: return launch(norm_bwd_kernel<T, 1, 4, 2, false, true>, g, f, smem, p, layer, st);
-    case 16: return launch(norm_bwd_kernel<T, 1, 8, 1, false, true>, g, f, smem, p, layer, st);
-    default: return launch(norm_bwd_kernel<T, 1, 14, 1, false, false>, g, f, smem, p, layer, st);
+    case 2: return launch(norm_bwd_kernel<T, 1, 1, 4, false, true, 112, false>, g, f, smem, p, layer, st);
+    case 8: return launch(norm_bwd_kernel<T, 1, 4, 2, false, true, 112, false>, g, f, smem, p, layer, st);
+    case 16: return launch(norm_bwd_kernel<T, 1, 8, 1, false, true, 128, false>, g, f, smem, p, layer, st);
+    default: return launch(norm_bwd_kernel<T, 1, 14, 1, false, false, 128, false>, g, f, smem, p, layer, st);
   }
 }
 
@@ -1000,7 +1002,7 @@ int lora_norm_fwd(const wp_mat* X, const wp_mat* weight, const wp_mat* bias, int
   if (Y->rows != X->rows || Y->cols != X->cols) return WP_ERR_SHAPE;
   if (weight && !valid_vec(weight, X->cols)) return weight->data ? WP_ERR_SHAPE : WP_ERR_INVALID;
   if (bias && !valid_vec(bias, X->cols)) return bias->data ? WP_ERR_SHAPE : WP_ERR_INVALID;
-  if (X->cols > 0x3FFFFFFFLL) return WP_ERR_UNSUPPORTED;
+  if (X->cols > 0x3FFFFFFFLL || X->rows > 0x7FFFFFFFLL) return WP_ERR_UNSUPPORTED;
   if (X->rows == 0) return WP_OK;
   NormParams p{};
   p.T = X->rows; p.C = static_cast<int>(X->cols);
@@ -1043,7 +1045,7 @@ int lora_norm_bwd(const wp_mat* dY, const wp_mat* X, const wp_mat* weight, const
     if (o->dtype != WP_FP32) return WP_ERR_DTYPE;
     if (o->rows * o->cols != X->cols) return WP_ERR_SHAPE;
   }
-  if (X->cols > 0x3FFFFFFFLL) return WP_ERR_UNSUPPORTED;
+  if (X->cols > 0x3FFFFFFFLL || X->rows > 0x7FFFFFFFLL) return WP_ERR_UNSUPPORTED;
   const bool sums = dW || dB;
   const size_t need = sums ? norm_bwd_workspace(X->rows, X->cols, X->dtype == WP_FP32) : 0;
   if (need > 0 && (!workspace || workspace_bytes < need)) return WP_ERR_WORKSPACE;
