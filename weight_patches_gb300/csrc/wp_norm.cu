@@ -427,19 +427,30 @@ __device__ __forceinline__ void store_sums(float* row, const Chunk<V>& x, int c,
   }
 }
 
-// The chunks of a weight or bias vector that a thread's columns need; kHold: kept in registers for
-// all rows, else loaded again at each use (where they would not fit beside the row).
-template <int V, int NC, bool kHold>
+// The chunks of a weight or bias vector that a thread's columns need: kept in registers for all rows
+// as values (kHeldValues) or, for bf16 vectors that would not fit beside the rows as values, packed
+// as loaded (kHeldPacked, V = 8); or loaded again at each use (kHeldNot), which exposes a load's
+// latency every turn.
+enum { kHeldNot = 0, kHeldValues = 1, kHeldPacked = 2 };
+template <int V, int NC, int kHeld>
 struct Held {
-  Chunk<V> c[kHold ? NC : 1];
+  Chunk<V> c[kHeld == kHeldValues ? NC : 1];
+  RawChunk<uint16_t, V> r[kHeld == kHeldPacked ? NC : 1];
   const void* p;
   int f32, vec, C;
   float none;                            // what a missing vector stands for (1 or 0)
   __device__ __forceinline__ Held(const void* p_, int f32_, int vec_, int C_, float none_)
       : p(p_), f32(f32_), vec(vec_), C(C_), none(none_) {
-    if (kHold)
 #pragma unroll
-      for (int i = 0; i < (kHold ? NC : 1); ++i) c[i] = load(i);
+    for (int i = 0; i < NC; ++i) {
+      if (kHeld == kHeldValues) c[kHeld == kHeldValues ? i : 0] = load(i);
+      if constexpr (kHeld == kHeldPacked && V == 8) {
+        const uint32_t w = none != 0.f ? 0x3f803f80u : 0u;
+        uint4 q = make_uint4(w, w, w, w);
+        if (p && chunk_col<V>(i) < C) q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + chunk_col<V>(i)));
+        r[i].u[0] = q.x; r[i].u[1] = q.y; r[i].u[2] = q.z; r[i].u[3] = q.w;
+      }
+    }
   }
   __device__ __forceinline__ Chunk<V> load(int i) const {
     Chunk<V> o;
@@ -448,7 +459,10 @@ struct Held {
     for (int k = 0; k < Chunk<V>::kPairs; ++k) o.p[k] = f2(none, none);
     return o;
   }
-  __device__ __forceinline__ Chunk<V> at(int i) const { return kHold ? c[kHold ? i : 0] : load(i); }
+  __device__ __forceinline__ Chunk<V> at(int i) const {
+    if constexpr (kHeld == kHeldPacked) return r[i].values();
+    else return kHeld == kHeldValues ? c[kHeld == kHeldValues ? i : 0] : load(i);
+  }
 };
 
 // The span of row j of a turn (V = 1): a padded row lies wholly in its slot.
@@ -464,7 +478,7 @@ __device__ __forceinline__ RowSpan<T, V> span_of(const Walk<T, V, ROWS, OPS>& wa
 
 // Forward, ROWS rows of a CTA per turn (a CTA is one warp where that is enough); NC chunks a thread,
 // all of which exist in every thread when kExact.
-template <typename T, int V, int NC, int ROWS, bool kHold, int kRegs, bool kExact>
+template <typename T, int V, int NC, int ROWS, int kHeld, int kRegs, bool kExact>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_fwd_kernel(const NormParams p, const bool layer) {
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[2][16 * ROWS];
@@ -473,7 +487,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_fwd_kerne
   constexpr int P = Chunk<V>::kPairs;
   Walk<T, V, ROWS, 1> walk(p, ring_mem, full);
   walk.begin(&abort_word);
-  const Held<V, NC, kHold> w(p.w, p.w_f32, p.w_vec, p.C, 1.f), b(p.b, p.b_f32, p.b_vec, p.C, 0.f);
+  const Held<V, NC, kHeld> w(p.w, p.w_f32, p.w_vec, p.C, 1.f), b(p.b, p.b_f32, p.b_vec, p.C, 0.f);
   auto have = [&](int i) { return kExact || chunk_col<V>(i) < p.C; };
   T* y = static_cast<T*>(p.y) + walk.row * p.ldy;
   const long long y_step = walk.step * p.ldy;
@@ -607,7 +621,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_long_kernel(const NormPa
 // Backward, ROWS rows of a CTA per turn; NC chunks a thread.  Between the sums and dx a thread keeps
 // xh and h of its columns, or (kRaw, where those and dw, db would not fit its registers) the raw
 // elements, and forms them again.
-template <typename T, int V, int NC, int ROWS, bool kRaw, bool kHold, int kRegs, bool kExact>
+template <typename T, int V, int NC, int ROWS, bool kRaw, int kHeld, int kRegs, bool kExact>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kernel(const NormParams p, const bool layer) {
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[2][16 * 2 * ROWS];
@@ -617,7 +631,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kerne
   Walk<T, V, ROWS, 2> walk(p, ring_mem, full);
   walk.begin(&abort_word);
   auto have = [&](int i) { return kExact || chunk_col<V>(i) < p.C; };
-  const Held<V, NC, kHold> wh(p.w, p.w_f32, p.w_vec, p.C, 1.f);
+  const Held<V, NC, kHeld> wh(p.w, p.w_f32, p.w_vec, p.C, 1.f);
   Chunk<V> dw[NC], db[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
@@ -847,7 +861,7 @@ Form fwd_form(long long C, bool f32, bool vec) {
   const long long n = vec ? C / (f32 ? 4 : 8) : C;
   Form f{0, 1, kMaxThreads, 64, 2, 0, 0};
   if (C > (1 << 20)) return f;
-  struct { int nv, rows, top, regs; } const vecs[] = {{1, 4, 64, 104}, {2, 4, 512, 112}, {4, 2, 512, 112}, {8, 1, 512, 128}},
+  struct { int nv, rows, top, regs; } const vecs[] = {{1, 4, 64, 104}, {2, 4, 512, 128}, {4, 2, 512, 128}, {8, 1, 512, 128}},
                                             ones[] = {{2, 4, 64, 64}, {8, 4, 384, 96}, {16, 2, 512, 112}, {32, 1, 512, 96}};
   for (int i = 0; i < 4; ++i) {
     const auto& q = vec ? vecs[i] : ones[i];
@@ -916,23 +930,28 @@ int dispatch_fwd(NormParams p, bool vec, bool layer, cudaStream_t st) {
   const size_t smem = static_cast<size_t>(f.stages) * f.rows * f.slot;
   const int g = blocks_of(p.T, f);
   const bool exact = vec && p.C == f.nv * f.threads * V;
+  const bool packed = (!p.w || (!p.w_f32 && p.w_vec)) && (!p.b || (!p.b_f32 && p.b_vec));
 #define WP_FWD(...) \
   (exact ? launch(norm_fwd_kernel<T, V, __VA_ARGS__, true>, g, f, smem, p, layer, st) \
          : launch(norm_fwd_kernel<T, V, __VA_ARGS__, false>, g, f, smem, p, layer, st))
   if (vec) {
     switch (f.nv) {
-      case 1: return WP_FWD(1, 4, true, 104);
-      case 2: return WP_FWD(2, 4, false, 112);
-      case 4: return WP_FWD(4, 2, false, 112);
-      default: return WP_FWD(8, 1, false, 128);
+      case 1: return WP_FWD(1, 4, kHeldValues, 104);
+      case 2:
+        if constexpr (V == 4) return WP_FWD(2, 4, kHeldValues, 112);
+        else return packed ? WP_FWD(2, 4, kHeldPacked, 128) : WP_FWD(2, 4, kHeldNot, 128);
+      case 4:
+        if constexpr (V == 4) return WP_FWD(4, 2, kHeldValues, 128);
+        else return packed ? WP_FWD(4, 2, kHeldPacked, 128) : WP_FWD(4, 2, kHeldNot, 128);
+      default: return WP_FWD(8, 1, kHeldNot, 128);
     }
   }
 #undef WP_FWD
   switch (f.nv) {                        // two elements a chunk
-    case 2: return launch(norm_fwd_kernel<T, 1, 1, 4, true, 64, false>, g, f, smem, p, layer, st);
-    case 8: return launch(norm_fwd_kernel<T, 1, 4, 4, true, 96, false>, g, f, smem, p, layer, st);
-    case 16: return launch(norm_fwd_kernel<T, 1, 8, 2, true, 112, false>, g, f, smem, p, layer, st);
-    default: return launch(norm_fwd_kernel<T, 1, 16, 1, false, 96, false>, g, f, smem, p, layer, st);
+    case 2: return launch(norm_fwd_kernel<T, 1, 1, 4, kHeldValues, 64, false>, g, f, smem, p, layer, st);
+    case 8: return launch(norm_fwd_kernel<T, 1, 4, 4, kHeldValues, 96, false>, g, f, smem, p, layer, st);
+    case 16: return launch(norm_fwd_kernel<T, 1, 8, 2, kHeldValues, 112, false>, g, f, smem, p, layer, st);
+    default: return launch(norm_fwd_kernel<T, 1, 16, 1, kHeldNot, 96, false>, g, f, smem, p, layer, st);
   }
 }
 
@@ -954,17 +973,17 @@ int dispatch_bwd(NormParams p, bool vec, bool layer, int* grid, cudaStream_t st)
          : launch(norm_bwd_kernel<T, V, __VA_ARGS__, false>, g, f, smem, p, layer, st))
   if (vec) {
     switch (f.nv) {
-      case 1: return WP_BWD(1, 4, false, true, 128);
-      case 2: return WP_BWD(2, 1, false, true, 128);
-      default: return WP_BWD(4, 1, sizeof(T) == 2, false, 128);
+      case 1: return WP_BWD(1, 4, false, kHeldValues, 128);
+      case 2: return WP_BWD(2, 1, false, kHeldValues, 128);
+      default: return WP_BWD(4, 1, sizeof(T) == 2, kHeldNot, 128);
     }
   }
 #undef WP_BWD
   switch (f.nv) {                        // two elements a chunk
-    case 2: return launch(norm_bwd_kernel<T, 1, 1, 4, false, true, 112, false>, g, f, smem, p, layer, st);
-    case 8: return launch(norm_bwd_kernel<T, 1, 4, 2, false, true, 112, false>, g, f, smem, p, layer, st);
-    case 16: return launch(norm_bwd_kernel<T, 1, 8, 1, false, true, 128, false>, g, f, smem, p, layer, st);
-    default: return launch(norm_bwd_kernel<T, 1, 14, 1, false, false, 128, false>, g, f, smem, p, layer, st);
+    case 2: return launch(norm_bwd_kernel<T, 1, 1, 4, false, kHeldValues, 112, false>, g, f, smem, p, layer, st);
+    case 8: return launch(norm_bwd_kernel<T, 1, 4, 2, false, kHeldValues, 112, false>, g, f, smem, p, layer, st);
+    case 16: return launch(norm_bwd_kernel<T, 1, 8, 1, false, kHeldValues, 128, false>, g, f, smem, p, layer, st);
+    default: return launch(norm_bwd_kernel<T, 1, 14, 1, false, kHeldNot, 128, false>, g, f, smem, p, layer, st);
   }
 }
 
