@@ -163,20 +163,33 @@ constexpr int kMaxThreads = 512;
 constexpr int kMaxStages = 8;
 constexpr int kSmemPerSm = 220 * 1024;
 
-// Pairs of float32.  (The packed f32x2 instructions halve the arithmetic but cost more in moves that
-// bring unpacked bf16 values into register pairs: 5 integer instructions an element against 3 fp32
-// ones saved, the 1536-wide forward 61 us against 41.)
+// f32x2: two float32 operations in one instruction
 struct F2 {
-  float x, y;
+  unsigned long long v;
 };
-__device__ __forceinline__ F2 f2(float a, float b) { return F2{a, b}; }
-__device__ __forceinline__ void f2_get(F2 a, float& x, float& y) {
-  x = a.x;
-  y = a.y;
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ F2 f2_add(F2 a, F2 b) { return F2{a.x + b.x, a.y + b.y}; }
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) { return F2{a.x * b.x, a.y * b.y}; }
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) { return F2{fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)}; }
+__device__ __forceinline__ void f2_get(F2 a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
 
 // A thread's columns come in chunks: one vector of V elements, or (V = 1) the two elements of
 // vectors 2 i and 2 i + 1; a chunk's values are pairs.
@@ -630,6 +643,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kerne
   constexpr int P = Chunk<V>::kPairs;
   Walk<T, V, ROWS, 2> walk(p, ring_mem, full);
   walk.begin(&abort_word);
+  if (threadIdx.x == 0) grid_launch_dependents();     // the column sums' second kernel may take its place
   auto have = [&](int i) { return kExact || chunk_col<V>(i) < p.C; };
   const Held<V, NC, kHeld> wh(p.w, p.w_f32, p.w_vec, p.C, 1.f);
   Chunk<V> dw[NC], db[NC];
@@ -661,7 +675,6 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kerne
       mu[j] = mu_n[j];
       r[j] = r_n[j];
     }
-    if (walk.total() - walk.row > walk.step) stats_of(walk.row + walk.step);
     fail = !mbar_wait(&full[walk.s], walk.phase, &abort_word, p.timeout_ns, p.status);
     walk.pad();
     Chunk<V> x[ROWS][kRaw ? 1 : NC], h[ROWS][kRaw ? 1 : NC];     // xh and dy w
@@ -703,6 +716,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kerne
     }
     cta_sum<2 * ROWS>(sums, red[odd], fail);   // every thread has read the stage; `fail` is the CTA's
     if (!fail) walk.refill();
+    if (walk.total() - walk.row > walk.step) stats_of(walk.row + walk.step);
     if (p.y) {
       const int rows = walk.total() - walk.row;
 #pragma unroll
@@ -791,24 +805,32 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_long_kernel(const NormPa
   }
 }
 
-// dw, db [C] from the CTAs' partial rows: 32 columns a block, 8 warps take every eighth
-// partial row, joined in warp order.
-__global__ void __launch_bounds__(256) norm_finish_kernel(const float* part, int n, int C, float* dw, float* db) {
-  __shared__ float sh[8][33];
-  grid_dependency_wait();
+// dw, db [C] from the CTAs' partial rows: 32 columns a block, 16 warps take every sixteenth partial
+// row, joined in warp order.  Launched beside the backward (its blocks wait for it to finish).
+__global__ void __launch_bounds__(512) norm_finish_kernel(const float* part, int n, int C, float* dw, float* db) {
+  __shared__ float sh[16][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float* out = blockIdx.y ? db : dw;
+  grid_dependency_wait();
   if (!out) return;
+  const float* q = part + static_cast<long long>(blockIdx.y) * C + c;
   float s = 0.f;
-  if (c < C)
-    for (int i = warp; i < n; i += 8) s += part[(static_cast<long long>(i) * 2 + blockIdx.y) * C + c];
+  if (c < C) {
+    for (int i0 = warp; i0 < n; i0 += 16 * 8) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = i0 + 16 * k < n ? q[static_cast<long long>(i0 + 16 * k) * 2 * C] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
+  }
   sh[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < C) {
     float t = sh[0][lane];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t += sh[i][lane];
+    for (int i = 1; i < 16; ++i) t += sh[i][lane];
     out[c] = t;
   }
 }
@@ -877,15 +899,17 @@ Form fwd_form(long long C, bool f32, bool vec) {
   return f;
 }
 
-// Backward: fewer elements a thread (its dw, db, weight, xh and h take registers each).
+// Backward: 8 elements a thread and four rows a turn (its dw, db, weight, xh and h take registers
+// each), 16 and two, or 32 and one.
 Form bwd_form(long long C, bool f32, bool vec) {
   const long long n = vec ? C / (f32 ? 4 : 8) : C;
   Form f{0, 1, kMaxThreads, 64, 2, 0, 0};
   if (C > (1 << 20)) return f;
-  struct { int nv, rows, top, regs; } const vecs[] = {{1, 4, 384, 128}, {2, 1, 384, 128}, {4, 1, 512, 128}, {4, 1, 512, 128}},
-                                            ones[] = {{2, 4, 256, 112}, {8, 2, 288, 112}, {16, 1, 512, 128}, {28, 1, 512, 128}};
+  struct { int nv, rows, top, regs; } const v8[] = {{1, 4, 512, 128}, {2, 2, 512, 128}, {4, 1, 512, 128}, {4, 1, 512, 128}},
+                                            v4[] = {{2, 4, 512, 128}, {4, 2, 512, 128}, {8, 1, 512, 128}, {8, 1, 512, 128}},
+                                            ones[] = {{2, 4, 256, 112}, {8, 2, 288, 112}, {16, 1, 512, 112}, {28, 1, 512, 128}};
   for (int i = 0; i < 4; ++i) {
-    const auto& q = vec ? vecs[i] : ones[i];
+    const auto& q = !vec ? ones[i] : f32 ? v4[i] : v8[i];
     if (n <= static_cast<long long>(q.nv) * q.top) {
       f.nv = q.nv;
       f.rows = q.rows;
@@ -968,21 +992,30 @@ int dispatch_bwd(NormParams p, bool vec, bool layer, int* grid, cudaStream_t st)
   p.slot = f.slot;
   const size_t smem = static_cast<size_t>(f.stages) * f.rows * 2 * f.slot;
   const bool exact = vec && p.C == f.nv * f.threads * V;
+  const bool packed = !p.w || (!p.w_f32 && p.w_vec);
 #define WP_BWD(...) \
-  (exact ? launch(norm_bwd_kernel<T, V, __VA_ARGS__, true>, g, f, smem, p, layer, st) \
-         : launch(norm_bwd_kernel<T, V, __VA_ARGS__, false>, g, f, smem, p, layer, st))
+  (exact ? launch(norm_bwd_kernel<T, V, __VA_ARGS__, 128, true>, g, f, smem, p, layer, st) \
+         : launch(norm_bwd_kernel<T, V, __VA_ARGS__, 128, false>, g, f, smem, p, layer, st))
   if (vec) {
-    switch (f.nv) {
-      case 1: return WP_BWD(1, 4, false, kHeldValues, 128);
-      case 2: return WP_BWD(2, 1, false, kHeldValues, 128);
-      default: return WP_BWD(4, 1, sizeof(T) == 2, kHeldNot, 128);
+    if constexpr (V == 8) {
+      switch (f.nv) {
+        case 1: return WP_BWD(1, 4, false, kHeldValues);
+        case 2: return packed ? WP_BWD(2, 2, false, kHeldPacked) : WP_BWD(2, 2, false, kHeldNot);
+        default: return packed ? WP_BWD(4, 1, true, kHeldPacked) : WP_BWD(4, 1, true, kHeldNot);
+      }
+    } else {
+      switch (f.nv) {
+        case 2: return WP_BWD(2, 4, false, kHeldValues);
+        case 4: return WP_BWD(4, 2, false, kHeldValues);
+        default: return WP_BWD(8, 1, false, kHeldNot);
+      }
     }
   }
 #undef WP_BWD
   switch (f.nv) {                        // two elements a chunk
     case 2: return launch(norm_bwd_kernel<T, 1, 1, 4, false, kHeldValues, 112, false>, g, f, smem, p, layer, st);
     case 8: return launch(norm_bwd_kernel<T, 1, 4, 2, false, kHeldValues, 112, false>, g, f, smem, p, layer, st);
-    case 16: return launch(norm_bwd_kernel<T, 1, 8, 1, false, kHeldValues, 128, false>, g, f, smem, p, layer, st);
+    case 16: return launch(norm_bwd_kernel<T, 1, 8, 1, false, kHeldValues, 112, false>, g, f, smem, p, layer, st);
     default: return launch(norm_bwd_kernel<T, 1, 14, 1, false, kHeldNot, 128, false>, g, f, smem, p, layer, st);
   }
 }
@@ -1108,8 +1141,13 @@ int lora_norm_bwd(const wp_mat* dY, const wp_mat* X, const wp_mat* weight, const
   if (rc != WP_OK || !sums) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.C + 31) / 32, 2);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(512);
   cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_finish_kernel, static_cast<const float*>(p.part), grid, p.C,
                                            dW ? static_cast<float*>(dW->data) : nullptr,
                                            dB ? static_cast<float*>(dB->data) : nullptr);
