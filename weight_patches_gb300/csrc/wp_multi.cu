@@ -5,8 +5,8 @@
 // (sglang PR, Motivation: the adapter and its scale belong to the request, so a batch meets
 // many of them.)  The adapters of a layer lie in a bank, one per slot, and every row names its
 // slot on the device.  This file holds the entry point: its checks, its workspace and the choice
-// between the two forms -- a few rows, where the weights' bytes are the work (wp_multi_small.cu),
-// and many (the blocks' slots and H~ in wp_multi_shrink.cu, then the fused forward of wp_tc_fwd.cu
+// between the forms -- a few rows, where the weights' bytes are the work (wp_multi_small.cu; with a
+// 4-bit weight the small-token kernels of wp_skinny.cu and wp_gemv.cu), and many (the blocks' slots and H~ in wp_multi_shrink.cu, then the fused forward of wp_tc_fwd.cu
 // with a lane mask per slot).
 #include <cmath>
 
@@ -48,11 +48,14 @@ int check(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
 
 // Rows up to which the weight-streaming kernels take a bf16 weight (or none).
 constexpr int kSmallRows = 128;
+// Rows up to which a 4-bit weight takes the small-token kernels.
+bool nf4_few(int T, const wp_mat* W) { return T <= kSkinnyMaxT && W && W->dtype == WP_NF4; }
 bool small_rows(int T, const wp_mat* W) { return T <= kSmallRows && (!W || W->dtype == WP_BF16); }
 
 // H~ [T, G R16] | act [T] (few rows), or s [T] | entries | their counts | rows with an adapter
+// the K splits' partial sums (a 4-bit weight, few rows) come last
 struct Layout {
-  size_t act = 0, ent = 0, ent_n = 0, ent_rows = 0, total = 0;
+  size_t act = 0, ent = 0, ent_n = 0, ent_rows = 0, part = 0, total = 0;
   int ent_ld = 0;
 };
 
@@ -66,7 +69,8 @@ Layout layout(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
     L.ent_ld = bank->n_slots < 256 ? bank->n_slots : 256;
     L.ent_n = L.ent + r256(blocks * L.ent_ld * sizeof(MultiEntry));
     L.ent_rows = L.ent_n + r256(blocks * 4);
-    L.total = L.ent_rows + r256(blocks * 32);
+    L.total = L.part = L.ent_rows + r256(blocks * 32);
+    if (nf4_few(static_cast<int>(T), W)) L.total += multi_skinny_bytes(X, W);
   }
   return L;
 }
@@ -133,6 +137,10 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
     rc = launch_multi_shrink_small(c, st);
     if (rc != WP_OK) return rc;
     return launch_multi_small(c, W ? W->data : nullptr, W ? W->ld : 0, st);
+  }
+  if (nf4_few(c.T, W)) {
+    rc = multi_skinny(c, X, W, bias, Y, ws + L.part, st);
+    if (rc != WP_ERR_UNSUPPORTED) return rc;
   }
   c.srow = reinterpret_cast<float*>(ws + L.act);
   c.ent = reinterpret_cast<MultiEntry*>(ws + L.ent);
