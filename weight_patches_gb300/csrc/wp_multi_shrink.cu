@@ -260,19 +260,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float s = row_ok ? c.srow[t] : 0.f;
     for (int u = 0; u < p.nc / 8 && ok; ++u) {
       uint32_t r8[8];
+      __syncwarp();
       if (kb1 > kb0) {
         tmem_ld8(tmem + lane_base + u * 8, r8);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) r8[i] = 0;
       }
+      const int j = j0 + u * 8;
       if (p.splits > 1) {
         float* o = part + row * (p.nc + 4) + u * 8;
         *reinterpret_cast<uint4*>(o) = make_uint4(r8[0], r8[1], r8[2], r8[3]);
         *reinterpret_cast<uint4*>(o + 4) = make_uint4(r8[4], r8[5], r8[6], r8[7]);
-      } else {
-        const int j = j0 + u * 8;
-        if (!row_ok || j >= rows) continue;
+      } else if (row_ok && j < rows) {
         const int g = j / c.R, r = j - g * c.R;
         uint16_t* h = c.H + static_cast<long long>(t) * c.G * c.R16 + g * c.R16 + r;
         auto f = [&](int i) { return __uint_as_float(r8[i]) * s; };
@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (c.R != c.R16 && r + 8 == c.R) st_global_v4(h + 8, 0, 0, 0, 0);   // the group's padding columns
       }
     }
+    __syncwarp();
     tc_fence_before();
   }
   __syncthreads();

@@ -13,10 +13,10 @@
 //           rather than tcgen05: there is no tile to keep, a row belongs to one slot only.
 //   main    W^T tiles of 128 output columns as the M = 128 operand of tcgen05.mma and the rows of
 //           X (rounded up to 16) as its width, W and X by TMA.  K is split over a cluster of up to
-//           8 CTAs so that two CTAs per SM are streaming W from the first moment; while they do,
-//           eight more warps form the adapters' term of the CTA's share of the rows on the CUDA
-//           cores (B is read once per row and the products are few: 2 R per output), and the
-//           partial tiles meet through distributed shared memory, added in CTA order.
+//           8 CTAs so that every SM is streaming W from the first moment; while they do, eight more
+//           warps form the adapters' term of the CTA's share of the rows, 16 output columns a warp,
+//           rows of one slot together up to 8 (the mma.sync fragments again, straight from global
+//           memory), and the partial tiles meet through distributed shared memory, added in CTA order.
 #include <atomic>
 
 #include <cuda.h>
@@ -52,7 +52,7 @@ constexpr int kMaxSmallT = 1024;          // rows a call of these kernels may ha
 // sums go to red[warp][16][8 NT].  U: 32-wide k steps whose loads are issued together.
 template <int NT, int U>
 __device__ __forceinline__ void shrink_pass(const MultiCall& c, const uint16_t* a_row0, const uint16_t* a_row1,
-                                            const int* list, int n, float* red) {
+                                            const int* list, int n, float* red, int part, int parts) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kl = (lane & 3) * 8;                   // this lane's 8 k of every 32
   const uint16_t* x[NT];
@@ -67,7 +67,7 @@ __device__ __forceinline__ void shrink_pass(const MultiCall& c, const uint16_t* 
 #pragma unroll
     for (int k = 0; k < 4; ++k) d[i][k] = 0.f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k0 = warp * (32 * U); k0 < c.K; k0 += kShrinkWarps * 32 * U) {
+  for (int k0 = (part * kShrinkWarps + warp) * (32 * U); k0 < c.K; k0 += parts * kShrinkWarps * 32 * U) {
     uint4 a0[U], a1[U], b[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -99,16 +99,19 @@ __device__ __forceinline__ void shrink_pass(const MultiCall& c, const uint16_t* 
   }
 }
 
-__global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(const MultiCall c) {
+// Grid: (rows x parts, chunks of 16 rank rows), a cluster of `parts` CTAs per (row, chunk) sharing K.
+__global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(const MultiCall c, const int parts) {
   __shared__ int list[kMaxSmallT];
   __shared__ int wcount[kShrinkWarps];
   __shared__ float red[kShrinkWarps * 16 * 32];
-  const int t = blockIdx.x, chunk = blockIdx.y;
+  __shared__ float sums[16 * 32];
+  const int t = static_cast<int>(blockIdx.x) / parts, chunk = blockIdx.y;
+  const int part = parts > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_launch_dependents();
   const int a = c.slot[t];
   if (a < 0 || a >= c.S) {
-    if (chunk == 0 && tid == 0) c.act[t] = -1;
+    if (chunk == 0 && part == 0 && tid == 0) c.act[t] = -1;
     return;
   }
   // the rows of this slot, in order; the first of them stands for the slot
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(cons
     earlier = earlier || (mine && j < t);
     const uint32_t m = __ballot_sync(0xffffffffu, mine);
     if (lane == 0) wcount[warp] = __popc(m);
-    if (__syncthreads_or(earlier)) return;
+    if (__syncthreads_or(earlier)) return;         // the same in every CTA of the cluster
     int at = n;
     for (int w = 0; w < kShrinkWarps; ++w) {
       if (w < warp) at += wcount[w];
@@ -140,29 +143,45 @@ __global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(cons
     const int left = n - p0;
     const int nt = left <= 8 ? 1 : 4;
     const int np = left < 8 * nt ? left : 8 * nt;
-    if (nt == 1) shrink_pass<1, 4>(c, a_row0, a_row1, list + p0, np, red);
-    else shrink_pass<4, 2>(c, a_row0, a_row1, list + p0, np, red);
+    if (nt == 1) shrink_pass<1, 4>(c, a_row0, a_row1, list + p0, np, red, part, parts);
+    else shrink_pass<4, 2>(c, a_row0, a_row1, list + p0, np, red, part, parts);
     __syncthreads();
     for (int i = tid; i < 16 * np; i += kShrinkThreads) {
       const int r = i / np, col = i - r * np;          // rank row of the chunk, row of the pass
-      const int j = j0 + r;
-      if (j >= rows) continue;
       float h = 0.f;
 #pragma unroll
       for (int w = 0; w < kShrinkWarps; ++w) h += red[(w * 16 + r) * (8 * nt) + col];
-      const int tt = list[p0 + col];
-      float s = sa;
-      if (c.row_scale) s = __fmul_rn(s, c.row_scale[tt]);
-      s = __fmul_rn(s, c.request_scale);
-      const int g = j / c.R, rr = j - g * c.R;
-      uint16_t* out = c.H + static_cast<long long>(tt) * c.G * c.R16 + g * c.R16 + rr;
-      uint16_t hb;
-      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(hb) : "f"(h * s));
-      *out = hb;
-      if (c.R != c.R16 && rr >= c.R - 8) out[8] = 0;   // the group's padding columns
-      if (j == 0) c.act[tt] = s != 0.f ? a : -1;
+      sums[r * 32 + col] = h;
     }
     __syncthreads();
+    if (parts > 1) cluster_sync();                     // every CTA's share of K is summed
+    if (part == 0) {
+      for (int i = tid; i < 16 * np; i += kShrinkThreads) {
+        const int r = i / np, col = i - r * np;
+        const int j = j0 + r;
+        if (j >= rows) continue;
+        float h = sums[r * 32 + col];
+        for (int q = 1; q < parts; ++q) {
+          float v;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                       : "=f"(v) : "r"(mapa_shared(smem_u32(&sums[r * 32 + col]), static_cast<uint32_t>(q))));
+          h += v;
+        }
+        const int tt = list[p0 + col];
+        float s = sa;
+        if (c.row_scale) s = __fmul_rn(s, c.row_scale[tt]);
+        s = __fmul_rn(s, c.request_scale);
+        const int g = j / c.R, rr = j - g * c.R;
+        uint16_t* out = c.H + static_cast<long long>(tt) * c.G * c.R16 + g * c.R16 + rr;
+        uint16_t hb;
+        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(hb) : "f"(h * s));
+        *out = hb;
+        if (c.R != c.R16 && rr >= c.R - 8) out[8] = 0;   // the group's padding columns
+        if (j == 0) c.act[tt] = s != 0.f ? a : -1;
+      }
+    }
+    __syncthreads();
+    if (parts > 1) cluster_sync();                     // the sums are read before they are written again
     p0 += np;
   }
 }
@@ -172,6 +191,7 @@ struct SmallMaps {
   CUtensorMap x, w;            // boxes of 64 K x t16 rows / 128 rows, 128-byte swizzle
 };
 
+constexpr int kMaxTile = 128;              // rows of X per tile at most
 constexpr int kSmallThreads = 384;         // warp 0 TMA, warp 1 MMA, warps 4..11 the adapters' term and the output
 constexpr int kSmallSmem = 113 * 1024 - 1024;   // two CTAs per SM
 constexpr int kSmallMaxStages = 8;
@@ -196,7 +216,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   uint8_t* sbase = smem_raw + (base_addr - raw_addr);
   float* part = reinterpret_cast<float*>(sbase);                       // [t16][128], over the drained stages
   float* delta = reinterpret_cast<float*>(sbase + p.stages * p.stage_bytes);   // [share][128]
-  int* act = reinterpret_cast<int*>(delta + p.share * 128);            // [share]
+  __shared__ int act[kMaxTile];                                        // the share's slots (-1: no adapter)
+  __shared__ int g_slot[kMaxTile], g_of[kMaxTile], g_count[4];         // groups of up to 8 rows of one slot
+  __shared__ uint8_t g_row[kMaxTile][8];
   __shared__ uint64_t full[kSmallMaxStages], empty[kSmallMaxStages], acc_full;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -225,6 +247,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   if (warp == 1) {
     tmem_alloc(&tmem_slot, p.tmem_cols);
     tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&maps.x);
+    if (p.has_w) tma_prefetch_desc(&maps.w);
   }
   tc_fence_before();
   __syncthreads();
@@ -283,54 +309,111 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     // ------------------------------------------------ the adapters' term of this CTA's rows
     const int row = (warp & 3) * 32 + lane;           // output column n0 + row = TMEM lane
     const int half = (warp - 4) >> 2;
-    const int n = n0 + row;
-    const bool n_ok = n < c.N;
     const int tid = threadIdx.x - 128;
-    grid_dependency_wait();                           // H~ and act
-    for (int i = tid; i < cnt; i += 256) act[i] = c.act[t0 + r0 + i];
+    // the share's rows in groups of up to 8 rows of one slot (the slots and scales are inputs: this
+    // runs beside the kernel that forms H~)
+    int a = -1;
+    if (tid < cnt) {
+      const int t = t0 + r0 + tid;
+      a = c.slot[t];
+      if (a < 0 || a >= c.S) {
+        a = -1;
+      } else {
+        float s = c.scale[a];
+        if (c.row_scale) s = __fmul_rn(s, c.row_scale[t]);
+        if (__fmul_rn(s, c.request_scale) == 0.f) a = -1;
+      }
+      act[tid] = a;
+    }
     named_bar_sync(1, 256);
-    const int g = n_ok ? n / c.og : 0;
-    const uint16_t* Hg = c.H + static_cast<long long>(t0 + r0) * c.G * c.R16 + g * c.R16;
+    int before = 0, lead = tid;                       // rows of this slot before this one; its group's first
+    if (a >= 0)
+      for (int j = 0; j < tid; ++j)
+        if (act[j] == a) {
+          if ((before & 7) == 0) lead = j;
+          ++before;
+        }
+    if ((before & 7) == 0) lead = tid;
+    const bool first = a >= 0 && lead == tid;
+    const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+    if (lane == 0 && warp < 8) g_count[warp - 4] = __popc(firsts);
+    named_bar_sync(1, 256);
+    int ng = 0, gid = __popc(firsts & ((1u << lane) - 1));
+    for (int w = 0; w < 4; ++w) {
+      if (w < warp - 4) gid += g_count[w];
+      ng += g_count[w];
+    }
+    if (first) {
+      g_slot[gid] = a;
+      g_of[tid] = gid;
+      *reinterpret_cast<uint2*>(g_row[gid]) = make_uint2(0xffffffffu, 0xffffffffu);
+    }
+    named_bar_sync(1, 256);
+    if (a >= 0) g_row[g_of[lead]][before & 7] = static_cast<uint8_t>(tid);
+    for (int i = half; i < cnt; i += 2)
+      if (act[i] < 0) delta[i * 128 + row] = 0.f;
+    named_bar_sync(1, 256);
+    // this warp's 16 output columns; the two halves may lie in different column groups
+    const int nw = n0 + (warp - 4) * 16;
+    const int n_lo = min(nw + (lane >> 2), c.N - 1), n_hi = min(nw + 8 + (lane >> 2), c.N - 1);
+    const int c_lo = min(nw, c.N - 1) / c.og, c_hi = min(nw + 8, c.N - 1) / c.og;
+    const int kl = (lane & 3) * 8;
     const int hld = c.G * c.R16;
-    constexpr int U = 4;
-    for (int i0 = half; i0 < cnt; i0 += 2 * U) {
-      const uint16_t* b[U];
-      const uint16_t* h[U];
-      float acc[U];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int g = 0; g < ng; ++g) {                    // pull the slots' columns of B toward L2 meanwhile
+      const uint16_t* b = c.B + (static_cast<long long>(g_slot[g]) * c.N + min(nw + (lane & 15), c.N - 1)) * c.R;
+      for (int o = (lane >> 4) * 64; o < c.R; o += 128) prefetch_l2(b + o);
+    }
+    grid_dependency_wait();                           // H~
+    constexpr int U = 2;                              // groups whose loads are issued together
+    for (int g0 = 0; g0 < ng; g0 += U) {
+      float d[U][4], e[U][4];
+      const uint16_t *b_lo[U], *b_hi[U], *h[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + 2 * u;
-        const int a = i < cnt && n_ok ? act[i] : -1;
-        acc[u] = 0.f;
-        b[u] = a >= 0 ? c.B + (static_cast<long long>(a) * c.N + n) * c.R : nullptr;
-        h[u] = Hg + static_cast<long long>(i < cnt ? i : 0) * hld;
+        const int g = min(g0 + u, ng - 1);
+        const long long sl = static_cast<long long>(g_slot[g]) * c.N;
+        b_lo[u] = c.B + (sl + n_lo) * c.R;
+        b_hi[u] = c.B + (sl + n_hi) * c.R;
+        const int tr = g_row[g][lane >> 2];
+        h[u] = tr < 255 ? c.H + static_cast<long long>(t0 + r0 + tr) * hld : nullptr;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[u][k] = e[u][k] = 0.f;
       }
-#pragma unroll 2
-      for (int r = 0; r < c.R; r += 8) {
-        uint4 bv[U], hv[U];
+      for (int q = 0; q < c.R; q += 32) {             // the whole warp: lanes past the rank add zeros
+        const int r = q + kl;
+        const bool ok = r < c.R;
+        uint4 lo[U], hi[U], h0[U], h1[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (b[u]) {
-            bv[u] = ldg16(b[u] + r);
-            hv[u] = *reinterpret_cast<const uint4*>(h[u] + r);
-          } else {
-            bv[u] = hv[u] = make_uint4(0, 0, 0, 0);
-          }
+          lo[u] = ok ? ldg16(b_lo[u] + r) : zero;
+          hi[u] = ok ? ldg16(b_hi[u] + r) : zero;
+          const bool hk = ok && h[u];
+          h0[u] = hk ? *reinterpret_cast<const uint4*>(h[u] + c_lo * c.R16 + r) : zero;
+          h1[u] = c_hi != c_lo && hk ? *reinterpret_cast<const uint4*>(h[u] + c_hi * c.R16 + r) : zero;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const uint32_t bw[4] = {bv[u].x, bv[u].y, bv[u].z, bv[u].w};
-          const uint32_t hw[4] = {hv[u].x, hv[u].y, hv[u].z, hv[u].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            acc[u] = fmaf(bf2f(hw[k] & 0xffffu), bf2f(bw[k] & 0xffffu), acc[u]);
-            acc[u] = fmaf(__uint_as_float(hw[k] & 0xffff0000u), __uint_as_float(bw[k] & 0xffff0000u), acc[u]);
+          mma_16816(d[u], lo[u].x, hi[u].x, lo[u].y, hi[u].y, h0[u].x, h0[u].y);
+          mma_16816(d[u], lo[u].z, hi[u].z, lo[u].w, hi[u].w, h0[u].z, h0[u].w);
+          if (c_hi != c_lo) {
+            mma_16816(e[u], lo[u].x, hi[u].x, lo[u].y, hi[u].y, h1[u].x, h1[u].y);
+            mma_16816(e[u], lo[u].z, hi[u].z, lo[u].w, hi[u].w, h1[u].z, h1[u].w);
           }
         }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + 2 * u < cnt) delta[(i0 + 2 * u) * 128 + row] = acc[u];
+      for (int u = 0; u < U; ++u) {
+        if (g0 + u >= ng) continue;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int tr = g_row[g0 + u][2 * (lane & 3) + k];
+          if (tr == 255) continue;
+          float* o = delta + tr * 128 + (warp - 4) * 16 + (lane >> 2);
+          o[0] = d[u][k];
+          o[8] = c_hi != c_lo ? e[u][2 + k] : d[u][2 + k];
+        }
+      }
     }
     // ------------------------------------------------ the accumulator into shared memory
     if (p.has_w) {
@@ -416,8 +499,23 @@ int fail(cudaError_t e) {
 }  // namespace
 
 int launch_multi_shrink_small(const MultiCall& c, cudaStream_t stream) {
-  multi_shrink_small_kernel<<<dim3(c.T, (c.G * c.R + 15) / 16), kShrinkThreads, 0, stream>>>(c);
-  const cudaError_t e = cudaGetLastError();
+  // a sweep of a CTA's warps covers 1024 of K; up to four CTAs share a longer K while the grid stays
+  // within two CTAs per SM
+  const int chunks = (c.G * c.R + 15) / 16;
+  int parts = 1;
+  while (parts < 4 && parts * 1024 < c.K && 2ll * parts * c.T * chunks <= 2ll * device_sm_count()) parts *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c.T * parts, chunks);
+  cfg.blockDim = dim3(kShrinkThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, multi_shrink_small_kernel, c, parts);
   return e == cudaSuccess ? WP_OK : fail(e);
 }
 
@@ -444,15 +542,24 @@ int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStr
     t_tiles = (c.T + p.tile - 1) / p.tile;
     p.t16 = (tile + 15) / 16 * 16;
     p.tmem_cols = p.t16 <= 32 ? 32 : (p.t16 <= 64 ? 64 : 128);
-    // K splits: the most (a power of two up to 8) that two CTAs per SM hold at once, each with at
-    // least two K blocks
+    // K splits (a cluster's CTAs, up to 8, each with at least two K blocks): the count whose busiest
+    // SM streams the least of K -- ceil(CTAs / SMs) / splits, the most splits on a tie.  Beyond 256
+    // CTAs the clusters no longer fit side by side: 64 rows of 5120 -> 5120 took 16.5 us with 6
+    // splits (240 CTAs), 22.6 with 7 (280) and 18.9 with 3 (120).
+    const long long tiles = static_cast<long long>(n_tiles) * t_tiles;
     p.splits = 1;
-    while (p.splits < 8 && 2ll * p.splits * n_tiles * t_tiles <= 2ll * device_sm_count() && p.k_blocks >= 4 * p.splits)
-      p.splits *= 2;
+    double best = 0;
+    for (int q = 1; q <= 8 && (q == 1 || (tiles * q <= 256 && p.k_blocks >= 2 * q)); ++q) {
+      const double load = static_cast<double>((tiles * q + device_sm_count() - 1) / device_sm_count()) / q;
+      if (q == 1 || load <= best) {
+        best = load;
+        p.splits = q;
+      }
+    }
     p.kb_per = (p.k_blocks + p.splits - 1) / p.splits;
     p.share = (tile + p.splits - 1) / p.splits;
     p.stage_bytes = kATileBytes + p.t16 * 128;
-    const int delta_bytes = p.share * (128 + 1) * 4 + 16;
+    const int delta_bytes = p.share * 128 * 4;
     p.stages = (kSmallSmem - 1024 - delta_bytes) / p.stage_bytes;
     if (p.stages > kSmallMaxStages) p.stages = kSmallMaxStages;
     if (p.stages > p.kb_per) p.stages = p.kb_per;
