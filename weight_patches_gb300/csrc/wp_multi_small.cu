@@ -192,7 +192,7 @@ struct SmallMaps {
 };
 
 constexpr int kMaxTile = 128;              // rows of X per tile at most
-constexpr int kSmallThreads = 384;         // warp 0 TMA, warp 1 MMA, warps 4..11 the adapters' term and the output
+constexpr int kSmallThreads = 320;         // warp 0 TMA, warp 1 MMA, warps 2..9 the adapters' term and the output
 constexpr int kSmallSmem = 113 * 1024 - 1024;   // two CTAs per SM
 constexpr int kSmallMaxStages = 8;
 
@@ -305,11 +305,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
         }
       }
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------ the adapters' term of this CTA's rows
     const int row = (warp & 3) * 32 + lane;           // output column n0 + row = TMEM lane
-    const int half = (warp - 4) >> 2;
-    const int tid = threadIdx.x - 128;
+    const int w8 = warp - 2;                          // 0..7
+    const int half = w8 >> 2;
+    const int tid = threadIdx.x - 64;
     // the share's rows in groups of up to 8 rows of one slot (the slots and scales are inputs: this
     // runs beside the kernel that forms H~)
     int a = -1;
@@ -336,11 +337,11 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     if ((before & 7) == 0) lead = tid;
     const bool first = a >= 0 && lead == tid;
     const uint32_t firsts = __ballot_sync(0xffffffffu, first);
-    if (lane == 0 && warp < 8) g_count[warp - 4] = __popc(firsts);
+    if (lane == 0 && w8 < 4) g_count[w8] = __popc(firsts);
     named_bar_sync(1, 256);
     int ng = 0, gid = __popc(firsts & ((1u << lane) - 1));
     for (int w = 0; w < 4; ++w) {
-      if (w < warp - 4) gid += g_count[w];
+      if (w < w8) gid += g_count[w];
       ng += g_count[w];
     }
     if (first) {
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
       if (act[i] < 0) delta[i * 128 + row] = 0.f;
     named_bar_sync(1, 256);
     // this warp's 16 output columns; the two halves may lie in different column groups
-    const int nw = n0 + (warp - 4) * 16;
+    const int nw = n0 + w8 * 16;
     const int n_lo = min(nw + (lane >> 2), c.N - 1), n_hi = min(nw + 8 + (lane >> 2), c.N - 1);
     const int c_lo = min(nw, c.N - 1) / c.og, c_hi = min(nw + 8, c.N - 1) / c.og;
     const int kl = (lane & 3) * 8;
@@ -364,57 +365,70 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
       const uint16_t* b = c.B + (static_cast<long long>(g_slot[g]) * c.N + min(nw + (lane & 15), c.N - 1)) * c.R;
       for (int o = (lane >> 4) * 64; o < c.R; o += 128) prefetch_l2(b + o);
     }
-    grid_dependency_wait();                           // H~
-    constexpr int U = 2;                              // groups whose loads are issued together
+    // Groups whose loads are issued together; the first ones' columns of B before the wait for H~.
+    constexpr int U = 4;
+    bool waited = false;
     for (int g0 = 0; g0 < ng; g0 += U) {
       float d[U][4], e[U][4];
-      const uint16_t *b_lo[U], *b_hi[U], *h[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int g = min(g0 + u, ng - 1);
-        const long long sl = static_cast<long long>(g_slot[g]) * c.N;
-        b_lo[u] = c.B + (sl + n_lo) * c.R;
-        b_hi[u] = c.B + (sl + n_hi) * c.R;
-        const int tr = g_row[g][lane >> 2];
-        h[u] = tr < 255 ? c.H + static_cast<long long>(t0 + r0 + tr) * hld : nullptr;
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int k = 0; k < 4; ++k) d[u][k] = e[u][k] = 0.f;
-      }
       for (int q = 0; q < c.R; q += 32) {             // the whole warp: lanes past the rank add zeros
         const int r = q + kl;
         const bool ok = r < c.R;
-        uint4 lo[U], hi[U], h0[U], h1[U];
+        uint4 lo[U], hi[U], h[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          lo[u] = ok ? ldg16(b_lo[u] + r) : zero;
-          hi[u] = ok ? ldg16(b_hi[u] + r) : zero;
-          const bool hk = ok && h[u];
-          h0[u] = hk ? *reinterpret_cast<const uint4*>(h[u] + c_lo * c.R16 + r) : zero;
-          h1[u] = c_hi != c_lo && hk ? *reinterpret_cast<const uint4*>(h[u] + c_hi * c.R16 + r) : zero;
+          const long long sl = static_cast<long long>(g_slot[min(g0 + u, ng - 1)]) * c.N;
+          lo[u] = ok ? ldg16(c.B + (sl + n_lo) * c.R + r) : zero;
+          hi[u] = ok ? ldg16(c.B + (sl + n_hi) * c.R + r) : zero;
         }
+        if (!waited) {
+          grid_dependency_wait();
+          waited = true;
+        }
+        auto load_h = [&](int cg) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int tr = g_row[min(g0 + u, ng - 1)][lane >> 2];
+            h[u] = ok && tr < 255
+                       ? *reinterpret_cast<const uint4*>(c.H + static_cast<long long>(t0 + r0 + tr) * hld + cg * c.R16 + r)
+                       : zero;
+          }
+        };
+        load_h(c_lo);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          mma_16816(d[u], lo[u].x, hi[u].x, lo[u].y, hi[u].y, h0[u].x, h0[u].y);
-          mma_16816(d[u], lo[u].z, hi[u].z, lo[u].w, hi[u].w, h0[u].z, h0[u].w);
-          if (c_hi != c_lo) {
-            mma_16816(e[u], lo[u].x, hi[u].x, lo[u].y, hi[u].y, h1[u].x, h1[u].y);
-            mma_16816(e[u], lo[u].z, hi[u].z, lo[u].w, hi[u].w, h1[u].z, h1[u].w);
+          mma_16816(d[u], lo[u].x, hi[u].x, lo[u].y, hi[u].y, h[u].x, h[u].y);
+          mma_16816(d[u], lo[u].z, hi[u].z, lo[u].w, hi[u].w, h[u].z, h[u].w);
+        }
+        if (c_hi != c_lo) {                           // (a warp's two halves in different column groups)
+          load_h(c_hi);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            mma_16816(e[u], lo[u].x, hi[u].x, lo[u].y, hi[u].y, h[u].x, h[u].y);
+            mma_16816(e[u], lo[u].z, hi[u].z, lo[u].w, hi[u].w, h[u].z, h[u].w);
           }
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (g0 + u >= ng) continue;
+        if (g0 + u < ng) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int tr = g_row[g0 + u][2 * (lane & 3) + k];
-          if (tr == 255) continue;
-          float* o = delta + tr * 128 + (warp - 4) * 16 + (lane >> 2);
-          o[0] = d[u][k];
-          o[8] = c_hi != c_lo ? e[u][2 + k] : d[u][2 + k];
+          for (int k = 0; k < 2; ++k) {
+            const int tr = g_row[g0 + u][2 * (lane & 3) + k];
+            if (tr < 255) {
+              float* o = delta + tr * 128 + w8 * 16 + (lane >> 2);
+              o[0] = d[u][k];
+              o[8] = c_hi != c_lo ? e[u][2 + k] : d[u][2 + k];
+            }
+          }
         }
       }
+      __syncwarp();
     }
+    if (!waited) grid_dependency_wait();
     // ------------------------------------------------ the accumulator into shared memory
     if (p.has_w) {
       const bool ok = mbar_wait(&acc_full, 0, abort_flag, tmo, status);
@@ -435,7 +449,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   }
   __syncthreads();
   if (p.splits > 1) cluster_sync();                   // every CTA's partial tile is in place
-  if (warp >= 4) {
+  if (warp >= 2) {
     // one row of X per warp, 4 output columns per lane: the splits' sums in CTA order
     const int n = n0 + lane * 4;
     float bias[4] = {0.f, 0.f, 0.f, 0.f};
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
       for (int k = 0; k < 4; ++k)
         bias[k] = c.bias_f32 ? static_cast<const float*>(c.bias)[n + k] : bf2f(static_cast<const uint16_t*>(c.bias)[n + k]);
     }
-    for (int i = warp - 4; i < cnt; i += 8) {
+    for (int i = warp - 2; i < cnt; i += 8) {
       float v[4] = {0.f, 0.f, 0.f, 0.f};
       if (p.has_w) {
         const uint32_t at = smem_u32(part + (r0 + i) * 128 + lane * 4);
