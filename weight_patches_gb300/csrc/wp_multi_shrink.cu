@@ -155,6 +155,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_relinquish();
   }
   if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&maps.x);
+      tma_prefetch_desc(&maps.a);
+    }
     // the slots of this half of the 256-row block
     grid_dependency_wait();
     const MultiEntry* ent = c.ent + static_cast<long long>(blk >> 1) * c.ent_ld;
@@ -188,22 +192,22 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 0) {
     if (lane == 0 && ne > 0) {
       const uint64_t keep = l2_evict_last();
-      uint32_t xi = 0, ai = 0;
+      // ring positions step along (a division by the ring's length would sit on the critical path);
+      // xp, ap: the parity of the slot's release that the next fill waits for
+      uint32_t xi = 0, ai = 0, xs = 0, as = 0, xp = 1, ap = 1;
       bool ok = true;
       for (int kb = kb0; kb < kb1 && ok; ++kb) {
-        const uint32_t s = xi % kXStages;
-        if (xi >= kXStages && !(ok = mbar_wait(&xempty[s], ((xi / kXStages) & 1u) ^ 1u, abort_flag, tmo, status))) break;
-        mbar_arrive_expect_tx(&xfull[s], kATileBytes);
-        tma_load_2d(sx + s * kATileBytes, &maps.x, kb * kBK, t0, &xfull[s]);
+        if (!(ok = mbar_wait(&xempty[xs], xp, abort_flag, tmo, status))) break;
+        mbar_arrive_expect_tx(&xfull[xs], kATileBytes);
+        tma_load_2d(sx + xs * kATileBytes, &maps.x, kb * kBK, t0, &xfull[xs]);
         ++xi;
+        if (++xs == kXStages) { xs = 0; xp ^= 1; }
         for (int e = 0; e < ne; ++e) {
-          const uint32_t q = ai % SA;
-          if (ai >= static_cast<uint32_t>(SA) &&
-              !(ok = mbar_wait(&aempty[q], ((ai / SA) & 1u) ^ 1u, abort_flag, tmo, status)))
-            break;
-          mbar_arrive_expect_tx(&afull[q], a_bytes);
-          tma_load_2d_hint(sa + q * a_bytes, &maps.a, kb * kBK, e_slot[e] * rows + j0, &afull[q], keep);
+          if (!(ok = mbar_wait(&aempty[as], ap, abort_flag, tmo, status))) break;
+          mbar_arrive_expect_tx(&afull[as], a_bytes);
+          tma_load_2d_hint(sa + as * a_bytes, &maps.a, kb * kBK, e_slot[e] * rows + j0, &afull[as], keep);
           ++ai;
+          if (++as == static_cast<uint32_t>(SA)) { as = 0; ap ^= 1; }
         }
       }
       if (!ok) {                                     // copies in flight land before the CTA leaves
@@ -221,26 +225,26 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16_f32(128, static_cast<uint32_t>(p.nc));
       const uint32_t ux = smem_u32(sx) >> 4, ua = smem_u32(sa) >> 4;
-      uint32_t xi = 0, ai = 0;
+      uint32_t xs = 0, as = 0, xp = 0, ap = 0;
       bool ok = true;
-      for (int kb = kb0; kb < kb1 && ok && ne > 0; ++kb, ++xi) {
-        const uint32_t s = xi % kXStages;
-        if (!(ok = mbar_wait(&xfull[s], (xi / kXStages) & 1u, abort_flag, tmo, status))) break;
-        const uint64_t ad = kDescSw128K | (ux + s * (kATileBytes >> 4));
-        for (int e = 0; e < ne; ++e, ++ai) {
-          const uint32_t q = ai % SA;
-          if (!(ok = mbar_wait(&afull[q], (ai / SA) & 1u, abort_flag, tmo, status))) break;
+      for (int kb = kb0; kb < kb1 && ok && ne > 0; ++kb) {
+        if (!(ok = mbar_wait(&xfull[xs], xp, abort_flag, tmo, status))) break;
+        const uint64_t ad = kDescSw128K | (ux + xs * (kATileBytes >> 4));
+        for (int e = 0; e < ne; ++e) {
+          if (!(ok = mbar_wait(&afull[as], ap, abort_flag, tmo, status))) break;
           tc_fence_after();
-          const uint64_t bd = kDescSw128K | (ua + q * (a_bytes >> 4));
+          const uint64_t bd = kDescSw128K | (ua + as * (a_bytes >> 4));
           const uint4 m = *reinterpret_cast<const uint4*>(e_off[e]);
           const uint32_t off[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
-            mma_bf16_lanes(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (xi > 0 || kk > 0) ? 1u : 0u, off);
-          mma_commit(&aempty[q]);
+            mma_bf16_lanes(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (kb > kb0 || kk > 0) ? 1u : 0u, off);
+          mma_commit(&aempty[as]);
+          if (++as == static_cast<uint32_t>(SA)) { as = 0; ap ^= 1; }
         }
         if (!ok) break;
-        mma_commit(&xempty[s]);
+        mma_commit(&xempty[xs]);
+        if (++xs == kXStages) { xs = 0; xp ^= 1; }
       }
       mma_commit(&acc_full);
       if (!ok) {

@@ -260,24 +260,23 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   if (warp == 0) {
     if (lane == 0 && p.has_w) {
       const uint64_t keep = l2_evict_last(), once = gridDim.y > 1 ? keep : l2_evict_first();
-      uint32_t issued = 0;
+      uint32_t issued = 0, s = 0, parity = 1;         // (a slot's first fill waits for no release)
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
-        const uint32_t s = issued % S;
-        if (issued >= static_cast<uint32_t>(S) &&
-            !(ok = mbar_wait(&empty[s], ((issued / S) & 1u) ^ 1u, abort_flag, tmo, status)))
-          break;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait(&empty[s], parity, abort_flag, tmo, status))) break;
         uint8_t* st = sbase + s * p.stage_bytes;
         mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(p.stage_bytes));
         tma_load_2d_hint(st, &maps.w, kb * kBK, n0, &full[s], once);
         tma_load_2d_hint(st + kATileBytes, &maps.x, kb * kBK, t0, &full[s], keep);
+        ++issued;
+        if (++s == static_cast<uint32_t>(S)) { s = 0; parity ^= 1; }
       }
       if (!ok)                                        // copies in flight land before the CTA leaves
-        for (uint32_t s = 0; s < static_cast<uint32_t>(S); ++s) {
-          const uint32_t uses = issued / S + (s < issued % S ? 1u : 0u);
+        for (uint32_t q = 0; q < static_cast<uint32_t>(S); ++q) {
+          const uint32_t uses = issued / S + (q < issued % S ? 1u : 0u);
           if (uses == 0) continue;
           const uint64_t b = globaltimer_ns();
-          while (!mbar_try_wait(smem_u32(&full[s]), (uses - 1) & 1u) && globaltimer_ns() - b < 100000000ull) {
+          while (!mbar_try_wait(smem_u32(&full[q]), (uses - 1) & 1u) && globaltimer_ns() - b < 100000000ull) {
           }
         }
     }
@@ -285,18 +284,18 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     if (lane == 0 && p.has_w) {
       const uint32_t idesc = idesc_bf16_f32(128, static_cast<uint32_t>(p.t16));
       const uint32_t u_w = smem_u32(sbase) >> 4;
-      uint32_t step = 0;
+      uint32_t s = 0, parity = 0, at = u_w;
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb, ++step) {
-        const uint32_t s = step % S;
-        if (!(ok = mbar_wait(&full[s], (step / S) & 1u, abort_flag, tmo, status))) break;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait(&full[s], parity, abort_flag, tmo, status))) break;
         tc_fence_after();
-        const uint32_t at = u_w + s * (static_cast<uint32_t>(p.stage_bytes) >> 4);
         const uint64_t ad = kDescSw128K | at, bd = kDescSw128K | (at + (kATileBytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < kBK / 16; ++kk)
-          mma_bf16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (step > 0 || kk > 0) ? 1u : 0u);
+          mma_bf16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
         mma_commit(&empty[s]);
+        at += static_cast<uint32_t>(p.stage_bytes) >> 4;
+        if (++s == static_cast<uint32_t>(S)) { s = 0; parity ^= 1; at = u_w; }
       }
       mma_commit(&acc_full);
       if (!ok) {                                      // the MMAs issued finish before tensor memory is freed
