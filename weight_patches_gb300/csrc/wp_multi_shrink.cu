@@ -3,14 +3,15 @@
 //
 // The rows of a batch come in the scheduler's order: long runs of one slot in prompts, any mixture
 // among decoding rows.  Nothing is sorted or copied: a tile of 128 rows of X is multiplied by the
-// rank rows of every slot it holds, and tcgen05.mma's lane mask keeps each slot's product in its
-// own rows of the accumulator, so one [128, rank] accumulator ends with each row's own X A^T.
-// A block inside one run costs one product per K step; a block of d slots costs d, and the traffic
-// that no order can avoid, d slots' A, each once per block.
+// rank rows of every slot it holds, as many slots side by side as one MMA (N <= 256) and the A ring
+// hold -- a small MMA costs its issue, 150 cycles, whatever its width -- and tcgen05.mma's lane mask
+// keeps each such group's product in its own rows of the accumulator, where a row's own slot is
+// one of the group's column ranges.  A block inside one run costs one product per K step; the
+// traffic that no order can avoid is d slots' A, each once per block.
 //
-// Bound by HBM on X while the blocks hold few slots (96 rank rows: 96 FLOP per byte of X), by the
-// MMA rate of d N = 16..128 products per K step otherwise.  Per CTA: warp 0 TMA (X and A in rings of
-// their own, since a K step of X serves every slot's A), warp 1 the MMAs, warps 2..5 the output.
+// Bound by HBM on X while the blocks hold few slots (96 rank rows: 96 FLOP per byte of X).  Per CTA:
+// warp 0 TMA (X and A in rings of their own, since a K step of X serves every group's A), warp 1
+// the MMAs, warps 2..5 the output.
 // K is split over a cluster when the blocks do not fill the SMs; the partial sums meet in
 // distributed shared memory and are added in CTA order.
 #include <atomic>
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(256) multi_plan_kernel(const MultiCall c) {
 constexpr int kThreads = 192;
 constexpr int kXStages = 3;
 constexpr int kMaxAStages = 16;
-constexpr int kSmem = 113 * 1024 - 1024;      // two CTAs per SM
+constexpr int kSmem = 108 * 1024;             // two CTAs per SM, 5 KiB of static arrays each beside it
 
 struct ShrinkMaps {
   CUtensorMap x;               // boxes of 64 K x 128 rows
@@ -104,9 +105,9 @@ struct ShrinkParams {
   MultiCall c;
   int nc;                      // rank rows per CTA (a multiple of 16, at most 128)
   int splits, kb_per, k_blocks;
-  int a_stages;
-  uint32_t tmem_cols;
+  int a_area;                  // bytes of the A ring
 };
+constexpr uint32_t kTmemCols = 256;           // two CTAs per SM
 
 __global__ void __launch_bounds__(kThreads, 2)
     multi_shrink_kernel(const __grid_constant__ ShrinkMaps maps, const __grid_constant__ ShrinkParams p) {
@@ -120,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ uint64_t xfull[kXStages], xempty[kXStages], afull[kMaxAStages], aempty[kMaxAStages], acc_full;
   __shared__ int e_slot[128];
   __shared__ __align__(16) uint32_t e_off[128][4];      // read and written 16 bytes at a time
+  __shared__ __align__(16) uint32_t g_off[128][4];      // the groups': the lanes that none of its slots owns
   __shared__ int e_n;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -132,8 +134,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int j0 = static_cast<int>(blockIdx.y) * p.nc;          // first rank row
   const int rows = c.G * c.R;
   const int kb0 = rank * p.kb_per, kb1 = min(p.k_blocks, kb0 + p.kb_per);
-  const uint32_t a_bytes = static_cast<uint32_t>(p.nc) * 128;
-  const int SA = p.a_stages;
+  const uint32_t a_bytes = static_cast<uint32_t>(p.nc) * 128;  // one slot's rank rows of a K step
   const uint64_t tmo = c.timeout_ns;
   int* status = c.status;
 
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], 1);
     }
-    for (int s = 0; s < SA; ++s) {
+    for (int s = 0; s < kMaxAStages; ++s) {
       mbar_init(&afull[s], 1);
       mbar_init(&aempty[s], 1);
     }
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(&tmem_slot, p.tmem_cols);
+    tmem_alloc(&tmem_slot, kTmemCols);
     tmem_relinquish();
   }
   if (warp == 0) {
@@ -181,6 +182,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       kept += __popc(b);
     }
     if (lane == 0) e_n = kept;
+    __syncwarp();
+    const int gs = max(1, min(min(256 / p.nc, p.a_area / (2 * p.nc * 128)), kept));
+    for (int g = lane; g * gs < kept; g += 32) {
+      uint4 m = make_uint4(~0u, ~0u, ~0u, ~0u);
+      for (int e = g * gs; e < min(kept, (g + 1) * gs); ++e) {
+        const uint4 q = *reinterpret_cast<const uint4*>(e_off[e]);
+        m.x &= q.x; m.y &= q.y; m.z &= q.z; m.w &= q.w;
+      }
+      *reinterpret_cast<uint4*>(g_off[g]) = m;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -188,6 +199,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == 0) grid_launch_dependents();
   const uint32_t tmem = tmem_slot;
   const int ne = e_n;
+  // gs slots form a group (one MMA per 16 of K): the most that one MMA's width and half of the A
+  // ring hold; SA ring slots of a group each
+  int gs = min(min(256 / p.nc, p.a_area / (2 * static_cast<int>(a_bytes))), ne);
+  gs = max(gs, 1);
+  const int groups = (ne + gs - 1) / gs;
+  const uint32_t g_bytes = gs * a_bytes;
+  const int SA = min(kMaxAStages, p.a_area / static_cast<int>(g_bytes));
 
   if (warp == 0) {
     if (lane == 0 && ne > 0) {
@@ -202,10 +220,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         tma_load_2d(sx + xs * kATileBytes, &maps.x, kb * kBK, t0, &xfull[xs]);
         ++xi;
         if (++xs == kXStages) { xs = 0; xp ^= 1; }
-        for (int e = 0; e < ne; ++e) {
+        for (int e = 0; e < ne; e += gs) {
           if (!(ok = mbar_wait(&aempty[as], ap, abort_flag, tmo, status))) break;
-          mbar_arrive_expect_tx(&afull[as], a_bytes);
-          tma_load_2d_hint(sa + as * a_bytes, &maps.a, kb * kBK, e_slot[e] * rows + j0, &afull[as], keep);
+          const int n = min(gs, ne - e);
+          mbar_arrive_expect_tx(&afull[as], n * a_bytes);
+          for (int i = 0; i < n; ++i)
+            tma_load_2d_hint(sa + as * g_bytes + i * a_bytes, &maps.a, kb * kBK, e_slot[e + i] * rows + j0, &afull[as],
+                             keep);
           ++ai;
           if (++as == static_cast<uint32_t>(SA)) { as = 0; ap ^= 1; }
         }
@@ -223,19 +244,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(128, static_cast<uint32_t>(p.nc));
+      const uint32_t idesc_g = idesc_bf16_f32(128, static_cast<uint32_t>(gs * p.nc));
+      const uint32_t idesc_l = idesc_bf16_f32(128, static_cast<uint32_t>((ne - (groups - 1) * gs) * p.nc));
       const uint32_t ux = smem_u32(sx) >> 4, ua = smem_u32(sa) >> 4;
       uint32_t xs = 0, as = 0, xp = 0, ap = 0;
       bool ok = true;
       for (int kb = kb0; kb < kb1 && ok && ne > 0; ++kb) {
         if (!(ok = mbar_wait(&xfull[xs], xp, abort_flag, tmo, status))) break;
         const uint64_t ad = kDescSw128K | (ux + xs * (kATileBytes >> 4));
-        for (int e = 0; e < ne; ++e) {
+        for (int g = 0; g < groups; ++g) {
           if (!(ok = mbar_wait(&afull[as], ap, abort_flag, tmo, status))) break;
           tc_fence_after();
-          const uint64_t bd = kDescSw128K | (ua + as * (a_bytes >> 4));
-          const uint4 m = *reinterpret_cast<const uint4*>(e_off[e]);
+          const uint64_t bd = kDescSw128K | (ua + as * (g_bytes >> 4));
+          const uint4 m = *reinterpret_cast<const uint4*>(g_off[g]);
           const uint32_t off[4] = {m.x, m.y, m.z, m.w};
+          const uint32_t idesc = g + 1 < groups ? idesc_g : idesc_l;
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
             mma_bf16_lanes(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (kb > kb0 || kk > 0) ? 1u : 0u, off);
@@ -254,35 +277,42 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   } else {
-    // thread = row of the block (its tensor-memory lane)
+    // thread = row of the block (its tensor-memory lane); the row's slot is number `mine` of its group
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full, 0, abort_flag, tmo, status)) && ne > 0;
-    tc_fence_after();
     const int t = t0 + row;
-    const bool row_ok = t < c.T;
-    const float s = row_ok ? c.srow[t] : 0.f;
-    for (int u = 0; u < p.nc / 8 && ok; ++u) {
-      uint32_t r8[8];
-      __syncwarp();
-      if (kb1 > kb0) {
-        tmem_ld8(tmem + lane_base + u * 8, r8);
-      } else {
+    int mine = -1;
+    for (int e = 0; e < ne; ++e)
+      if (!((e_off[e][row >> 5] >> (row & 31)) & 1u)) mine = e % gs;
+    const float s = t < c.T ? c.srow[t] : 0.f;
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full, 0, abort_flag, tmo, status));
+    tc_fence_after();
+    for (int i = 0; i < gs && ok && ne > 0; ++i) {
+      if (__ballot_sync(0xffffffffu, mine == i) == 0) continue;     // (uniform)
+      for (int u = 0; u < p.nc / 8; ++u) {
+        uint32_t r8[8];
+        __syncwarp();
+        if (kb1 > kb0) {
+          tmem_ld8(tmem + lane_base + i * p.nc + u * 8, r8);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r8[i] = 0;
-      }
-      const int j = j0 + u * 8;
-      if (p.splits > 1) {
-        float* o = part + row * (p.nc + 4) + u * 8;
-        *reinterpret_cast<uint4*>(o) = make_uint4(r8[0], r8[1], r8[2], r8[3]);
-        *reinterpret_cast<uint4*>(o + 4) = make_uint4(r8[4], r8[5], r8[6], r8[7]);
-      } else if (row_ok && j < rows) {
-        const int g = j / c.R, r = j - g * c.R;
-        uint16_t* h = c.H + static_cast<long long>(t) * c.G * c.R16 + g * c.R16 + r;
-        auto f = [&](int i) { return __uint_as_float(r8[i]) * s; };
-        st_global_v4(h, pack_bf16x2(f(0), f(1)), pack_bf16x2(f(2), f(3)), pack_bf16x2(f(4), f(5)),
-                     pack_bf16x2(f(6), f(7)));
-        if (c.R != c.R16 && r + 8 == c.R) st_global_v4(h + 8, 0, 0, 0, 0);   // the group's padding columns
+          for (int k = 0; k < 8; ++k) r8[k] = 0;
+        }
+        const int j = j0 + u * 8;
+        if (mine == i) {
+          if (p.splits > 1) {
+            float* o = part + row * (p.nc + 4) + u * 8;
+            *reinterpret_cast<uint4*>(o) = make_uint4(r8[0], r8[1], r8[2], r8[3]);
+            *reinterpret_cast<uint4*>(o + 4) = make_uint4(r8[4], r8[5], r8[6], r8[7]);
+          } else if (j < rows) {
+            const int g = j / c.R, r = j - g * c.R;
+            uint16_t* h = c.H + static_cast<long long>(t) * c.G * c.R16 + g * c.R16 + r;
+            auto f = [&](int k) { return __uint_as_float(r8[k]) * s; };
+            st_global_v4(h, pack_bf16x2(f(0), f(1)), pack_bf16x2(f(2), f(3)), pack_bf16x2(f(4), f(5)),
+                         pack_bf16x2(f(6), f(7)));
+            if (c.R != c.R16 && r + 8 == c.R) st_global_v4(h + 8, 0, 0, 0, 0);   // the group's padding columns
+          }
+        }
       }
     }
     __syncwarp();
@@ -297,18 +327,23 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int row = rank * share + i / units, u = i % units;
       const int t = t0 + row, j = j0 + u * 8;
       if (t >= c.T || j >= rows) continue;
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      float4 a[8][2];                                  // every split's loads before the first sum
       const uint32_t at = smem_u32(part + row * (p.nc + 4) + u * 8);
-      for (int q = 0; q < p.splits; ++q) {
-        float a[8];
-        const uint32_t ra = mapa_shared(at, static_cast<uint32_t>(q));
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]) : "r"(ra));
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7]) : "r"(ra + 16));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += a[k];
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t ra = mapa_shared(at, static_cast<uint32_t>(min(q, p.splits - 1)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                       : "=f"(a[q][h].x), "=f"(a[q][h].y), "=f"(a[q][h].z), "=f"(a[q][h].w) : "r"(ra + 16 * h));
       }
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < p.splits) {
+          v[0] += a[q][0].x; v[1] += a[q][0].y; v[2] += a[q][0].z; v[3] += a[q][0].w;
+          v[4] += a[q][1].x; v[5] += a[q][1].y; v[6] += a[q][1].z; v[7] += a[q][1].w;
+        }
       const float s = c.srow[t];
       const int g = j / c.R, r = j - g * c.R;
       uint16_t* h = c.H + static_cast<long long>(t) * c.G * c.R16 + g * c.R16 + r;
@@ -324,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, p.tmem_cols);
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -356,19 +391,15 @@ int launch_multi_shrink(const MultiCall& c, cudaStream_t stream) {
   const int rows16 = (c.G * c.R + 15) / 16 * 16;
   const int chunks = (rows16 + 127) / 128;
   p.nc = ((rows16 + chunks - 1) / chunks + 15) / 16 * 16;
-  p.tmem_cols = p.nc <= 32 ? 32 : (p.nc <= 64 ? 64 : 128);
   p.k_blocks = (c.K + kBK - 1) / kBK;
   const int blocks = (c.T + 127) / 128;
   p.splits = 1;
   while (p.splits < 8 && 2ll * p.splits * blocks * chunks <= 2ll * device_sm_count() && p.k_blocks >= 4 * p.splits)
     p.splits *= 2;
   p.kb_per = (p.k_blocks + p.splits - 1) / p.splits;
-  const int a_bytes = p.nc * 128;
-  p.a_stages = (kSmem - 1024 - kXStages * kATileBytes) / a_bytes;
-  if (p.a_stages > kMaxAStages) p.a_stages = kMaxAStages;
-  const size_t smem = 1024 + kXStages * kATileBytes + static_cast<size_t>(p.a_stages) * a_bytes;
-  // the partial sums [128][nc + 4] lie over the rings: 48 KiB of X and at least 2 tiles of A hold them
-  if (static_cast<size_t>(128) * (p.nc + 4) * 4 > smem - 1024) return WP_ERR_UNSUPPORTED;
+  p.a_area = (kSmem - 1024 - kXStages * kATileBytes) / 1024 * 1024;
+  const size_t smem = 1024 + kXStages * kATileBytes + static_cast<size_t>(p.a_area);
+  // the partial sums [128][nc + 4] lie over the rings (nc <= 128: 66 KiB of 107)
   ShrinkMaps maps{};
   int rc = encode_map_bf16(&maps.x, c.X, c.K, c.T, c.ldx, kBK, 128, 128);
   if (rc == WP_OK)

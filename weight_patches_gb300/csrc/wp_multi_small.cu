@@ -193,7 +193,7 @@ struct SmallMaps {
 
 constexpr int kMaxTile = 128;              // rows of X per tile at most
 constexpr int kSmallThreads = 320;         // warp 0 TMA, warp 1 MMA, warps 2..9 the adapters' term and the output
-constexpr int kSmallSmem = 113 * 1024 - 1024;   // two CTAs per SM
+constexpr int kSmallSmem = 109 * 1024;     // two CTAs per SM, 3 KiB of static arrays each beside it
 constexpr int kSmallMaxStages = 8;
 
 struct SmallParams {
