@@ -46,8 +46,10 @@ int check(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
   return WP_OK;
 }
 
-// Rows up to which the weight-streaming kernels take a bf16 weight (or none).
-constexpr int kSmallRows = 128;
+// Rows up to which the weight-streaming kernels take a bf16 weight (or none).  At 256 rows they took
+// 27-60 us on five layers (1536 -> 4608 and 8960, 4096^2, 5120^2, 8960 -> 1536; 8-16 slots in any order, in runs
+// or one) where the masked fused forward took 28-111; at 512 rows of one slot 28-69 against 29-66.
+constexpr int kSmallRows = 256;
 // Rows up to which a 4-bit weight takes the small-token kernels.
 bool nf4_few(int T, const wp_mat* W) { return T <= kSkinnyMaxT && W && W->dtype == WP_NF4; }
 bool small_rows(int T, const wp_mat* W) { return T <= kSmallRows && (!W || W->dtype == WP_BF16); }

@@ -6,7 +6,7 @@
 // handful of products, so HBM is the floor and the start-up of each kernel the next bound.  Two
 // kernels, the second started while the first runs (programmatic dependent launch):
 //
-//   shrink  one CTA per (slot present, 16 rank rows): its 8 warps take turns along K with loads
+//   shrink  one CTA per (32 rows of one slot, 16 rank rows): its 8 warps take turns along K with loads
 //           straight from global into mma.sync fragments -- the rank rows are the 16-row operand,
 //           the slot's rows of X the 8-wide one, both through the same permutation of k so that
 //           every lane loads 16 consecutive bytes -- and leave H~ = bf16(s X A^T).  mma.sync
@@ -114,24 +114,25 @@ __global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(cons
     if (chunk == 0 && part == 0 && tid == 0) c.act[t] = -1;
     return;
   }
-  // the rows of this slot, in order; the first of them stands for the slot
-  int n = 0;
-  bool earlier = false;
+  // the rows of this slot in order, 32 to a pass; the first of each pass stands for it
+  int before = 0, n = 0;
   for (int base = 0; base < c.T; base += kShrinkThreads) {
     const int j = base + tid;
     const bool mine = j < c.T && c.slot[j] == a;
-    earlier = earlier || (mine && j < t);
-    const uint32_t m = __ballot_sync(0xffffffffu, mine);
-    if (lane == 0) wcount[warp] = __popc(m);
-    if (__syncthreads_or(earlier)) return;         // the same in every CTA of the cluster
-    int at = n;
+    const uint32_t m = __ballot_sync(0xffffffffu, mine), em = __ballot_sync(0xffffffffu, mine && j < t);
+    if (lane == 0) wcount[warp] = __popc(m) | __popc(em) << 16;
+    __syncthreads();
+    int at = n;                                      // this slot's rows before this warp's
     for (int w = 0; w < kShrinkWarps; ++w) {
-      if (w < warp) at += wcount[w];
-      n += wcount[w];
+      if (w < warp) at += wcount[w] & 0xffff;
+      n += wcount[w] & 0xffff;
+      before += wcount[w] >> 16;
     }
     if (mine) list[at + __popc(m & ((1u << lane) - 1))] = j;
     __syncthreads();
   }
+  if (before % 32) return;                           // the same in every CTA of the cluster
+  n = min(n - before, 32);
   const int rows = c.G * c.R;
   const int j0 = chunk * 16;
   const uint16_t* A = c.A + static_cast<long long>(a) * rows * c.K;
@@ -139,27 +140,24 @@ __global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(cons
   const uint16_t* a_row0 = A + static_cast<long long>(min(j0 + (lane >> 2), rows - 1)) * c.K;
   const uint16_t* a_row1 = A + static_cast<long long>(min(j0 + 8 + (lane >> 2), rows - 1)) * c.K;
   const float sa = c.scale[a];
-  for (int p0 = 0; p0 < n;) {
-    const int left = n - p0;
-    const int nt = left <= 8 ? 1 : 4;
-    const int np = left < 8 * nt ? left : 8 * nt;
-    if (nt == 1) shrink_pass<1, 4>(c, a_row0, a_row1, list + p0, np, red, part, parts);
-    else shrink_pass<4, 2>(c, a_row0, a_row1, list + p0, np, red, part, parts);
-    __syncthreads();
-    for (int i = tid; i < 16 * np; i += kShrinkThreads) {
-      const int r = i / np, col = i - r * np;          // rank row of the chunk, row of the pass
-      float h = 0.f;
+  const int nt = n <= 8 ? 1 : 4;
+  if (nt == 1) shrink_pass<1, 4>(c, a_row0, a_row1, list + before, n, red, part, parts);
+  else shrink_pass<4, 2>(c, a_row0, a_row1, list + before, n, red, part, parts);
+  __syncthreads();
+  for (int i = tid; i < 16 * n; i += kShrinkThreads) {
+    const int r = i / n, col = i - r * n;              // rank row of the chunk, row of the pass
+    float h = 0.f;
 #pragma unroll
-      for (int w = 0; w < kShrinkWarps; ++w) h += red[(w * 16 + r) * (8 * nt) + col];
-      sums[r * 32 + col] = h;
-    }
-    __syncthreads();
-    if (parts > 1) cluster_sync();                     // every CTA's share of K is summed
-    if (part == 0) {
-      for (int i = tid; i < 16 * np; i += kShrinkThreads) {
-        const int r = i / np, col = i - r * np;
-        const int j = j0 + r;
-        if (j >= rows) continue;
+    for (int w = 0; w < kShrinkWarps; ++w) h += red[(w * 16 + r) * (8 * nt) + col];
+    sums[r * 32 + col] = h;
+  }
+  __syncthreads();
+  if (parts > 1) cluster_sync();                       // every CTA's share of K is summed
+  if (part == 0) {
+    for (int i = tid; i < 16 * n; i += kShrinkThreads) {
+      const int r = i / n, col = i - r * n;
+      const int j = j0 + r;
+      if (j < rows) {
         float h = sums[r * 32 + col];
         for (int q = 1; q < parts; ++q) {
           float v;
@@ -167,7 +165,7 @@ __global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(cons
                        : "=f"(v) : "r"(mapa_shared(smem_u32(&sums[r * 32 + col]), static_cast<uint32_t>(q))));
           h += v;
         }
-        const int tt = list[p0 + col];
+        const int tt = list[before + col];
         float s = sa;
         if (c.row_scale) s = __fmul_rn(s, c.row_scale[tt]);
         s = __fmul_rn(s, c.request_scale);
@@ -180,10 +178,9 @@ __global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(cons
         if (j == 0) c.act[tt] = s != 0.f ? a : -1;
       }
     }
-    __syncthreads();
-    if (parts > 1) cluster_sync();                     // the sums are read before they are written again
-    p0 += np;
   }
+  __syncthreads();
+  if (parts > 1) cluster_sync();                       // no CTA leaves while its sums are read
 }
 
 // ------------------------------------------------------------------------------ main
@@ -513,10 +510,10 @@ int fail(cudaError_t e) {
 
 int launch_multi_shrink_small(const MultiCall& c, cudaStream_t stream) {
   // a sweep of a CTA's warps covers 1024 of K; up to four CTAs share a longer K while the grid stays
-  // within two CTAs per SM
+  // within eight CTAs per SM (most of a grid leaves at once where rows share slots)
   const int chunks = (c.G * c.R + 15) / 16;
   int parts = 1;
-  while (parts < 4 && parts * 1024 < c.K && 2ll * parts * c.T * chunks <= 2ll * device_sm_count()) parts *= 2;
+  while (parts < 4 && parts * 1024 < c.K && 2ll * parts * c.T * chunks <= 8ll * device_sm_count()) parts *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c.T * parts, chunks);
   cfg.blockDim = dim3(kShrinkThreads);
