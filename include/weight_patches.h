@@ -478,6 +478,7 @@ typedef struct wp_adamw_plan {
   int32_t n_tensors;
   int32_t n_launches;
   int64_t unit_begin[WP_ADAMW_MAX_LAUNCHES + 1];
+  uint32_t launches_8bit;  /* bit l: launch l has tensors with 8-bit moments */
 } wp_adamw_plan;
 
 /* The step's scalars.  g = grad * grad_scale (* grad_scale_dev[0] when not NULL: a clip or loss

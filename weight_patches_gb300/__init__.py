@@ -67,7 +67,7 @@ class WpAdamWTensor(ctypes.Structure):
 
 class WpAdamWPlan(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("n_tensors", ctypes.c_int32), ("n_launches", ctypes.c_int32),
-                ("unit_begin", ctypes.c_int64 * 17)]
+                ("unit_begin", ctypes.c_int64 * 17), ("launches_8bit", ctypes.c_uint32)]
 
 
 class WpAdamWArgs(ctypes.Structure):

@@ -40,6 +40,8 @@
 // Operands are K-major bf16 in the 128-byte swizzle layout.  Every wait (mbarrier or
 // flag) is bounded (wall clock); on expiry the CTA records WP_ERR_TIMEOUT, waits for its
 // own copies in flight, frees tensor memory and returns.
+#include <atomic>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1303,9 +1305,18 @@ int launch_tc_fwd(const TcMaps& maps, const TcParams& params, int grid, size_t s
              : launch_impl<false, false>(maps, p, grid, smem_bytes, stream);
 }
 
+// The status word's address on the current device, looked up once per device.
 int* tc_status_ptr() {
+  static std::atomic<int*> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  if (dev >= 0 && dev < 64) {
+    int* p = cached[dev].load(std::memory_order_relaxed);
+    if (p) return p;
+  }
   void* ptr = nullptr;
   if (cudaGetSymbolAddress(&ptr, g_tc_status) != cudaSuccess) return nullptr;
+  if (dev >= 0 && dev < 64) cached[dev].store(static_cast<int*>(ptr), std::memory_order_relaxed);
   return static_cast<int*>(ptr);
 }
 
