@@ -8,13 +8,25 @@
 // Both are bound by HBM.  Rows travel by bulk copies into a ring of row slots in shared memory,
 // several rows ahead, so that the bytes in flight do not depend on how many registers the
 // arithmetic takes; a row is then held in registers, its sums are taken there (the squares after
-// the mean is out, so that a large mean costs no digits), and it is written once.  Rows whose start
-// is not 16-byte aligned travel too: the aligned inside by the copy, the few elements around it
-// by plain loads.  The arithmetic runs on float32 pairs (two operations per instruction).
+// the mean is out, so that a large mean costs no digits), and it is written once.  The arithmetic runs
+// on float32 pairs (two operations per instruction).  Rows of any length and alignment travel the
+// same way: the copy takes the 16-byte pieces that hold them, each thread picks its vector of columns
+// out of two pieces, and on the way out shuffles bring the vectors back to 16-byte pieces.
 // Forward: a CTA works through its rows, one warp where a row is short.  Backward: a CTA's threads
 // keep their columns over all of its rows, so the column sums dw and db stay in registers; each
 // CTA leaves one partial row of them in the workspace, which a second kernel adds in order: no
 // atomics, the same bits each time.
+//
+// Measured (device time; bytes read and written once over it; a copy reaches 6.8 TB/s):
+//   32760 x 1536 bf16   forward 34 us, 5.9 TB/s; backward 65 us, 4.7 TB/s (of it 9 us until the first
+//                       rows are there and 5 us for the second kernel; between them 5.9 TB/s)
+//   8000 x 5120 fp32    forward 56 us, 5.9 TB/s; backward 83 us, 5.9 TB/s
+//   16 x 5120 bf16      forward 3.5 us, of which a launch is most
+//   20000 x 2187 bf16   forward 70 us, 2.5 TB/s; backward 161 us, 1.6 TB/s: the shifts, twice the
+//                       arithmetic of an aligned row, are what bounds these
+//   8000 x 4099 fp32    forward 93 us, 2.8 TB/s; backward 124 us, 3.2 TB/s
+// Shifted rows were read and written element by element first: 96 and 278 us, 102 and 161 us.  Their
+// backward takes half the rows a turn of an aligned one's: with as many, the registers spill (221 us).
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -163,22 +175,54 @@ constexpr int kMaxThreads = 512;
 constexpr int kMaxStages = 8;
 constexpr int kSmemPerSm = 220 * 1024;
 
-// A thread's columns come in chunks: one vector of V elements, or (V = 1) the two elements of
-// vectors 2 i and 2 i + 1; a chunk's values are pairs.
+// A thread's columns come in chunks of one vector of V elements; their values are pairs.
 template <int V>
 struct Chunk {
-  static constexpr int kPairs = V > 1 ? V / 2 : 1;
+  static constexpr int kPairs = V / 2;
   F2 p[kPairs];
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) p[k] = f2(0.f, 0.f);
   }
+  // the elements past the first n
+  __device__ __forceinline__ void cut(int n) {
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      float a, b;
+      f2_get(p[k], a, b);
+      p[k] = f2(2 * k < n ? a : 0.f, 2 * k + 1 < n ? b : 0.f);
+    }
+  }
 };
-// first column of chunk i, and of its second element when V = 1
-template <int V>
+
+// How the rows lie.  kExact: 16-byte aligned, and every thread has all of its chunks.  kWhole: aligned,
+// of whole vectors.  kShifted: any alignment and length.  There a warp's chunks are neighbours, so that
+// shuffles can bring a row's vectors to the 16-byte pieces that they are stored in.
+enum { kExact = 0, kWhole = 1, kShifted = 2 };
+
+// first column of chunk i of NC
+template <int V, int NC, int kMode>
 __device__ __forceinline__ int chunk_col(int i) {
-  return V > 1 ? (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V
-               : 2 * i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+  if (kMode == kShifted)
+    return ((static_cast<int>(threadIdx.x >> 5) * NC + i) * 32 + static_cast<int>(threadIdx.x & 31)) * V;
+  return (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V;
+}
+
+// The 16 bytes from byte `sh` (0 to 15, the same in a warp) of the first six of eight words, those
+// words taken from the eight by bit 3 already.
+template <typename T>
+__device__ __forceinline__ void window(const uint32_t (&b)[6], uint32_t sh, uint32_t (&o)[4]) {
+  uint32_t c[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) c[k] = sh & 4 ? b[k + 1] : b[k];
+  if (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = c[k];
+  } else {
+    const uint32_t sel = sh & 2 ? 0x5432u : 0x3210u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = __byte_perm(c[k], c[k + 1], sel);
+  }
 }
 
 __device__ __forceinline__ float f2_sum(F2 a) {
@@ -193,33 +237,50 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-// A row's 16-byte aligned inside, which travels by bulk copy into a slot at the same offset from a
-// 16-byte boundary; its first `head` and last `tail` elements (none in an aligned row) are read
-// from global memory by the threads that use them.
-template <typename T, int V>
+// What of rows r to r + n - 1, which lie one after another (or n is 1), travels by bulk copy: the 16-byte
+// pieces that hold them, into shared memory at the same offset from a 16-byte boundary.  The outermost
+// pieces reach into the rows before and after, so the matrix's first row leaves out its first piece
+// where that is not all its own, and the last row its last: those elements are patched in.  (At first
+// every row's ends were read from global memory: the wait for them, once a turn, took most of the time.)
+template <typename T>
 struct RowSpan {
   const T* row;
-  int off;                               // elements from the slot's start to the row's
-  int lo, hi;                            // columns [lo, hi) are in the slot
-  __device__ __forceinline__ RowSpan(const T* r, int C) : row(r) {
-    if (V > 1) {                         // aligned rows of whole vectors
-      off = lo = 0;
-      hi = C;
-      return;
+  int lo, hi;                            // elements [lo, hi) of the n C travel
+  uintptr_t from;                        // the copy's source and bytes
+  uint32_t skip;                         // bytes from the row's 16-byte boundary to the copy's start
+  uint32_t bytes;
+  __device__ __forceinline__ RowSpan(const T* base, long long ld, long long r, int n, long long rows, int C)
+      : row(base + r * ld) {
+    const int len = n * C;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(row), e = b + static_cast<uintptr_t>(len) * sizeof(T);
+    lo = 0;
+    hi = len;
+    skip = 0;
+    const bool tiny = ld * static_cast<long long>(sizeof(T)) < 16;
+    from = b & ~static_cast<uintptr_t>(15);
+    uintptr_t to = (e + 15) & ~static_cast<uintptr_t>(15);
+    if ((b & 15u) && (r == 0 || tiny)) {
+      from += 16;
+      skip = 16;
     }
-    const uintptr_t b = reinterpret_cast<uintptr_t>(r), e = b + static_cast<uintptr_t>(C) * sizeof(T);
-    off = static_cast<int>((b & 15u) / sizeof(T));
-    const uintptr_t ab = (b + 15) & ~static_cast<uintptr_t>(15), ae = e & ~static_cast<uintptr_t>(15);
-    lo = ae > ab ? static_cast<int>((ab - b) / sizeof(T)) : C;
-    hi = ae > ab ? static_cast<int>((ae - b) / sizeof(T)) : C;
+    if (r + n == rows || tiny) to = e & ~static_cast<uintptr_t>(15);
+    bytes = to > from ? static_cast<uint32_t>(to - from) : 0;
+    if (!bytes) {
+      lo = hi = len;
+    } else {
+      if (from > b) lo = static_cast<int>((from - b) / sizeof(T));
+      if (to < e) hi = static_cast<int>((to - b) / sizeof(T));
+    }
   }
 };
 
 // The CTA's walk: turn after turn of ROWS rows, through a ring of stages that each hold those rows
-// of OPS matrices (operand-major slots).  Thread 0 fills a stage with bulk copies; a stage may be
-// filled again once every thread has read it (the callers pass a CTA barrier in between).  Row
-// numbers are 32-bit, offsets 64-bit; pointers step from turn to turn.
-template <typename T, int V, int ROWS, int OPS>
+// of OPS matrices.  A stage is filled with bulk copies: one for the turn's rows of a matrix where they
+// lie one after another (they do in shared memory then, too), else one a row, into slots; kShifted
+// works its spans out a lane each (one thread took a microsecond a turn for them).  A stage may be
+// filled again once every thread has read it (the callers pass a CTA barrier in between).  Row numbers
+// are 32-bit, offsets 64-bit; pointers step from turn to turn.
+template <typename T, int kMode, int ROWS, int OPS>
 struct Walk {
   const NormParams& p;
   uint64_t* full;
@@ -234,6 +295,7 @@ struct Walk {
   __device__ __forceinline__ int total() const { return static_cast<int>(p.T); }
   __device__ __forceinline__ uint32_t stage_bytes() const { return static_cast<uint32_t>(p.slot) * (ROWS * OPS); }
   __device__ __forceinline__ bool more() const { return row < total(); }
+  __device__ __forceinline__ bool joined() const { return p.ldx == p.C && (OPS == 1 || p.lddy == p.C); }
   __device__ __forceinline__ void next() {
     row = total() - row > step ? row + step : total();
     base += stage_bytes();
@@ -243,60 +305,106 @@ struct Walk {
       base -= static_cast<uint32_t>(p.stages) * stage_bytes();
     }
   }
-  // shared-memory address of row j of operand o in this turn's stage
+  // shared-memory address of slot j of operand o in this turn's stage
   __device__ __forceinline__ uint32_t at(int j, int o) const {
     return base + static_cast<uint32_t>((o * ROWS + j) * p.slot);
+  }
+  __device__ __forceinline__ RowSpan<T> span(int o, long long r, int n) const {
+    return RowSpan<T>(static_cast<const T*>(o == 0 ? p.x : p.dy), o == 0 ? p.ldx : p.lddy, r, n, p.T, p.C);
   }
   __device__ __forceinline__ const T* src(int o, long long r) const {
     return o == 0 ? static_cast<const T*>(p.x) + r * p.ldx : static_cast<const T*>(p.dy) + r * p.lddy;
   }
-  // the rows from r0 (64-bit: it may lie past the end) into the stage at `dst` (thread 0)
+  // the rows from r0 (64-bit: it may lie past the end) into the stage at `dst` (warp 0)
   __device__ __forceinline__ void fill(uint32_t dst, int stage, long long r0) const {
     if (r0 >= p.T) return;
     const int n = p.T - r0 < ROWS ? static_cast<int>(p.T - r0) : ROWS;
-    uint64_t* bar = &full[stage];
-    uint32_t bytes = 0;
-    if (V > 1) {
-      bytes = static_cast<uint32_t>(n * OPS * p.C) * sizeof(T);
-    } else {
-      for (int o = 0; o < OPS; ++o)
-        for (int j = 0; j < n; ++j) {
-          const RowSpan<T, V> q(src(o, r0 + j), p.C);
-          bytes += static_cast<uint32_t>(q.hi - q.lo) * sizeof(T);
+    if constexpr (kMode != kShifted) {
+      if (threadIdx.x != 0) return;
+      mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(n * OPS * p.C) * sizeof(T));
+      for (int o = 0; o < OPS; ++o) {
+        const uint32_t d = dst + static_cast<uint32_t>(o * ROWS * p.slot);
+        if ((o == 0 ? p.ldx : p.lddy) == p.C) {
+          bulk_load(d, src(o, r0), static_cast<uint32_t>(n * p.C) * sizeof(T), &full[stage]);
+          continue;
         }
-    }
-    mbar_arrive_expect_tx(bar, bytes);
-    for (int o = 0; o < OPS; ++o) {
-      const uint32_t d = dst + static_cast<uint32_t>(o * ROWS * p.slot);
-      if (V > 1 && (o == 0 ? p.ldx : p.lddy) == p.C) {   // whole rows one after another: one copy
-        bulk_load(d, src(o, r0), static_cast<uint32_t>(n * p.C) * sizeof(T), bar);
-        continue;
+        for (int j = 0; j < n; ++j)
+          bulk_load(d + j * p.slot, src(o, r0 + j), static_cast<uint32_t>(p.C) * sizeof(T), &full[stage]);
       }
-      for (int j = 0; j < n; ++j) {
-        const RowSpan<T, V> q(src(o, r0 + j), p.C);
-        if (q.hi > q.lo)
-          bulk_load(d + j * p.slot + (q.off + q.lo) * static_cast<int>(sizeof(T)), q.row + q.lo,
-                    static_cast<uint32_t>(q.hi - q.lo) * sizeof(T), bar);
-      }
+      return;
     }
+    const int lane = threadIdx.x & 31;
+    const bool one = joined();
+    const int o = one ? lane : lane / ROWS, j = one ? 0 : lane % ROWS;
+    uint64_t* bar = &full[stage];
+    const bool mine = o < OPS && j < n;
+    const RowSpan<T> q = span(mine ? o : 0, r0 + (mine ? j : 0), one ? n : 1);
+    const uint32_t bytes = mine ? q.bytes : 0;
+    const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
+    if (lane == 0) mbar_arrive_expect_tx(bar, all);
+    __syncwarp();
+    if (bytes)
+      bulk_load(dst + static_cast<uint32_t>((o * ROWS + j) * p.slot) + q.skip, reinterpret_cast<const void*>(q.from), bytes,
+                bar);
   }
   __device__ __forceinline__ void refill() const {       // this turn's stage, `stages` turns on
-    if (threadIdx.x == 0) fill(base, s, row + static_cast<long long>(step) * p.stages);
+    if (threadIdx.x < (kMode == kShifted ? 32 : 1)) fill(base, s, row + static_cast<long long>(step) * p.stages);
   }
   // Barriers, then the first `stages` turns on their way.
   __device__ __forceinline__ void begin(volatile int* abort_flag) const {
-    if (threadIdx.x == 0) {
-      for (int i = 0; i < p.stages; ++i) mbar_init(&full[i], 1);
-      *abort_flag = 0;
-      fence_barrier_init();
-      fence_proxy_async_smem();
+    if (threadIdx.x < 32) {
+      if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) mbar_init(&full[i], 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
       for (int i = 0; i < p.stages; ++i) fill(base + i * stage_bytes(), i, row + static_cast<long long>(step) * i);
     }
+    __syncthreads();
+  }
+  // Shared-memory address of column 0 of row j of operand o (a row past the end: its slot's start, which
+  // lies behind the rows there are).
+  __device__ __forceinline__ uint32_t column0(int j, int o) const {
+    if (row + j >= total()) return at(j, o);
+    if (kMode != kShifted) return at(j, o);
+    const uint32_t pitch = static_cast<uint32_t>(p.C) * static_cast<uint32_t>(sizeof(T));
+    const bool one = joined();
+    const uint32_t a = one ? at(0, o) + static_cast<uint32_t>(j) * pitch : at(j, o);
+    const uint32_t b = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(o == 0 ? p.x : p.dy));
+    const uint32_t ld = static_cast<uint32_t>(o == 0 ? p.ldx : p.lddy);
+    return a + ((b + static_cast<uint32_t>(one ? row : row + j) * ld * static_cast<uint32_t>(sizeof(T))) & 15u);
+  }
+  // What the copies left out of the first and last rows, by plain loads (a CTA barrier in their turns
+  // only).
+  __device__ __forceinline__ void patch() const {
+    if (kMode != kShifted) return;
+    const bool tiny = (OPS == 2 && p.lddy < p.ldx ? p.lddy : p.ldx) * static_cast<long long>(sizeof(T)) < 16;
+    const int n = total() - row < ROWS ? total() - row : ROWS;
+    if (row != 0 && row + n != total() && !tiny) return;
+    const bool one = joined();
+    for (int o = 0; o < OPS; ++o)
+      for (int j = 0; j < (one ? 1 : n); ++j) {
+        const RowSpan<T> q = span(o, row + j, one ? n : 1);
+        const int len = one ? n * p.C : p.C;
+        for (int i = threadIdx.x; i < q.lo + len - q.hi; i += blockDim.x) {
+          const int c = i < q.lo ? i : q.hi + i - q.lo;
+          if (c >= len) break;
+          const uint32_t to = column0(j, o) + static_cast<uint32_t>(c) * static_cast<uint32_t>(sizeof(T));
+          if (sizeof(T) == 2)
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(reinterpret_cast<const uint16_t*>(q.row)[c]) : "memory");
+          else
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(reinterpret_cast<const uint32_t*>(q.row)[c]) : "memory");
+        }
+      }
+    fence_proxy_async_smem();            // the stage is filled by a copy again
     __syncthreads();
   }
   // The last turn may hold fewer than ROWS rows: the missing ones read as zeros, so that the turn
   // needs no tests (a CTA barrier in that turn only).
   __device__ __forceinline__ void pad() const {
+    patch();
     const int n = total() - row;
     if (n >= ROWS) return;
     for (int o = 0; o < OPS; ++o)
@@ -316,41 +424,31 @@ struct Walk {
   }
 };
 
-// One element of a row in its slot (or, outside the slot's span, in global memory)
-template <typename T>
-__device__ __forceinline__ float slot_at(uint32_t slot, const RowSpan<T, 1>& q, int c) {
-  if (c < q.lo || c >= q.hi) {
-    Raw<T, 1> r;
-    r.load(q.row + c);
-    return r.at(0);
-  }
-  const uint32_t a = slot + static_cast<uint32_t>(q.off + c) * static_cast<uint32_t>(sizeof(T));
-  if constexpr (sizeof(T) == 2) {
-    uint16_t h;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a));
-    return __uint_as_float(static_cast<uint32_t>(h) << 16);
-  } else {
-    float f;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a));
-    return f;
-  }
-}
-
-// Chunk i of a row, as loaded (V > 1: the raw vector; V = 1: two floats), and its values.  The
-// chunk's first column exists; a missing second element (V = 1) is zero.
+// Chunk i of a row as loaded, and its values.
 template <typename T, int V>
 struct RawChunk {
-  static constexpr int kWords = V > 1 ? 4 : 2;
-  uint32_t u[kWords];
-  __device__ __forceinline__ void load(uint32_t slot, const RowSpan<T, V>& q, int c, int C) {
-    if constexpr (V > 1) {
+  uint32_t u[4];
+  // from column c, at shared-memory address `at`; n columns exist from there on
+  template <int kMode>
+  __device__ __forceinline__ void load(uint32_t at, int n) {
+    if constexpr (kMode != kShifted) {
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                   : "r"(slot + static_cast<uint32_t>(c) * static_cast<uint32_t>(sizeof(T))));
+                   : "r"(at));
     } else {
-      const int c1 = c + static_cast<int>(blockDim.x);
-      u[0] = __float_as_uint(slot_at(slot, q, c));
-      u[1] = c1 < C ? __float_as_uint(slot_at(slot, q, c1)) : 0u;
+      uint32_t b[6];
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b[2 * k]), "=r"(b[2 * k + 1]) : "r"((at & ~7u) + 8 * k));
+      window<T>(b, at, u);
+      if (n < V) {
+        asm volatile("" ::: "memory");     // a branch that few warps take, not selects in all
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (sizeof(T) == 4) u[k] = k < n ? u[k] : 0u;
+          else u[k] = 2 * k + 1 < n ? u[k] : 2 * k < n ? u[k] & 0xffffu : 0u;
+        }
+      }
     }
   }
   __device__ __forceinline__ Chunk<V> values() const {
@@ -368,36 +466,121 @@ struct RawChunk {
 template <int V>
 __device__ __forceinline__ Chunk<V> vec_chunk(const void* p, int f32, int vec, int c, int C) {
   Chunk<V> o;
-  if constexpr (V > 1) {
-    float t[V];
+  float t[V];
+  if (c + V <= C) {
     load_vec<V>(p, f32, vec, c, t);
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k) o.p[k] = f2(t[2 * k], t[2 * k + 1]);
   } else {
-    float a[1], b[1] = {0.f};
-    const int c1 = c + static_cast<int>(blockDim.x);
-    load_vec<1>(p, f32, 0, c, a);
-    if (c1 < C) load_vec<1>(p, f32, 0, c1, b);
-    o.p[0] = f2(a[0], b[0]);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float q[1] = {0.f};
+      if (c + k < C) load_vec<1>(p, f32, 0, c + k, q);
+      t[k] = q[0];
+    }
   }
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) o.p[k] = f2(t[2 * k], t[2 * k + 1]);
   return o;
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void store_chunk(T* row, const Chunk<V>& x, int c, int C) {
-  if constexpr (V > 1) {
-    float o[V];
+__device__ __forceinline__ void store_chunk(T* row, const Chunk<V>& x, int c) {
+  float o[V];
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k) f2_get(x.p[k], o[2 * k], o[2 * k + 1]);
-    store_row<T, V>(row + c, o);
-  } else {
-    float a[1], b[1];
-    f2_get(x.p[0], a[0], b[0]);
-    const int c1 = c + static_cast<int>(blockDim.x);
-    store_row<T, 1>(row + c, a);
-    if (c1 < C) store_row<T, 1>(row + c1, b);
-  }
+  for (int k = 0; k < V / 2; ++k) f2_get(x.p[k], o[2 * k], o[2 * k + 1]);
+  store_row<T, V>(row + c, o);
 }
+
+// A row of any alignment, stored by a warp chunk after chunk (all lanes call for every chunk).  The row's
+// 16-byte piece at a vector's column holds the last s elements of the vector before it and the first
+// V - s of its own: the lane before gives its words (the last lane those of the chunk before).  At a
+// warp's two ends a piece is another warp's in part: each stores its part in 2, 4 and 8 bytes.  The
+// row's last piece goes element by element.
+template <typename T, int V, int NC, int kMode>
+struct ShiftedStore {
+  T* row;
+  uint32_t off;                          // bytes from a 16-byte boundary to column 0, and to any vector
+  int s;
+  uint32_t last[4];                      // the chunk before, of lane 31 (lane 0's neighbour)
+  __device__ __forceinline__ explicit ShiftedStore(T* r)
+      : row(r), off(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r)) & 15u),
+        s(static_cast<int>(off) / static_cast<int>(sizeof(T))) {}
+  __device__ __forceinline__ void shift(const uint32_t (&a)[8], uint32_t (&o)[4]) const {
+    const uint32_t sh = 16u - off;
+    uint32_t b[6];
+#pragma unroll
+    for (int k = 0; k < 6; ++k) b[k] = sh & 8 ? a[k + 2] : a[k];
+    window<T>(b, sh, o);
+  }
+  __device__ __forceinline__ void put(const Chunk<V>& x, int i, int C, bool live) {
+    const int lane = threadIdx.x & 31, c = chunk_col<V, NC, kMode>(i);
+    uint32_t a[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float x0, x1;
+      if constexpr (V == 8) {
+        f2_get(x.p[k], x0, x1);
+        a[4 + k] = pack_bf16x2(x0, x1);
+      } else {
+        f2_get(x.p[k >> 1], x0, x1);
+        a[4 + k] = __float_as_uint(k & 1 ? x1 : x0);
+      }
+    }
+    char* piece = reinterpret_cast<char*>(row + c) - off;
+    if (off == 0) {
+      if (live && c + V <= C) st_global_v4(piece, a[4], a[5], a[6], a[7]);
+      if (live && c + V > C) put_elements(a, c, 0, C - c);
+      return;
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t give = lane == 31 && i > 0 ? last[k] : a[4 + k];
+      a[k] = __shfl_sync(0xffffffffu, give, (lane + 31) & 31);
+      last[k] = a[4 + k];
+    }
+    shift(a, o);
+    const int left = C - (c - s);        // elements from the piece's first on
+    if (!live) return;
+    if ((lane > 0 || i > 0) && left >= V) st_global_v4(piece, o[0], o[1], o[2], o[3]);
+    if (i == 0 && lane == 0 && left >= V) {        // bytes [off, 16) of the piece
+      asm volatile("" ::: "memory");
+      if (sizeof(T) == 2 && (off & 2)) *reinterpret_cast<uint16_t*>(piece + off) = static_cast<uint16_t>(pick(o, off >> 2) >> 16);
+      const uint32_t w = (off + 3) >> 2;
+      if (w & 1) *reinterpret_cast<uint32_t*>(piece + 4 * w) = w == 1 ? o[1] : o[3];
+      if (w <= 2) *reinterpret_cast<uint2*>(piece + 8) = make_uint2(o[2], o[3]);
+    }
+    if (i == NC - 1 && lane == 31 && c + V <= C) { // bytes [0, off) of the next piece
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[k] = a[4 + k];
+      shift(a, o);
+      piece += 16;
+      if (off & 8) *reinterpret_cast<uint2*>(piece) = make_uint2(o[0], o[1]);
+      if (off & 4) *reinterpret_cast<uint32_t*>(piece + (off & 8)) = off & 8 ? o[2] : o[0];
+      if (sizeof(T) == 2 && (off & 2)) *reinterpret_cast<uint16_t*>(piece + (off & 12)) = static_cast<uint16_t>(pick(o, off >> 2));
+      return;
+    }
+    // the row's last vector: its elements in a piece that no vector store covers
+    const bool next = (lane < 31 || i < NC - 1) && left >= 2 * V;
+    if (left < V || !next) {
+      asm volatile("" ::: "memory");
+      put_elements(a, c, left < V ? 0 : V - s, C - c);
+    }
+  }
+  __device__ __forceinline__ static uint32_t pick(const uint32_t (&o)[4], uint32_t w) {
+    const uint32_t lo = w & 1 ? o[1] : o[0], hi = w & 1 ? o[3] : o[2];
+    return w & 2 ? hi : lo;
+  }
+  // own elements k with from <= k < n
+  __device__ __forceinline__ void put_elements(const uint32_t (&a)[8], int c, int from, int n) const {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (k < from || k >= n) continue;
+      if constexpr (V == 8) reinterpret_cast<uint16_t*>(row + c)[k] = static_cast<uint16_t>(a[4 + (k >> 1)] >> (16 * (k & 1)));
+      else reinterpret_cast<uint32_t*>(row + c)[k] = a[4 + k];
+    }
+  }
+};
 
 // A chunk of the partial column sums (rows of C floats, of any alignment)
 template <int V>
@@ -406,9 +589,8 @@ __device__ __forceinline__ void store_sums(float* row, const Chunk<V>& x, int c,
   for (int k = 0; k < Chunk<V>::kPairs; ++k) {
     float a, b;
     f2_get(x.p[k], a, b);
-    const int c1 = V > 1 ? c + 2 * k + 1 : c + static_cast<int>(blockDim.x);
-    row[V > 1 ? c + 2 * k : c] = a;
-    if (c1 < C) row[c1] = b;
+    if (c + 2 * k < C) row[c + 2 * k] = a;
+    if (c + 2 * k + 1 < C) row[c + 2 * k + 1] = b;
   }
 }
 
@@ -417,7 +599,7 @@ __device__ __forceinline__ void store_sums(float* row, const Chunk<V>& x, int c,
 // as loaded (kHeldPacked, V = 8); or loaded again at each use (kHeldNot), which exposes a load's
 // latency every turn.
 enum { kHeldNot = 0, kHeldValues = 1, kHeldPacked = 2 };
-template <int V, int NC, int kHeld>
+template <int V, int NC, int kHeld, int kMode>
 struct Held {
   Chunk<V> c[kHeld == kHeldValues ? NC : 1];
   RawChunk<uint16_t, V> r[kHeld == kHeldPacked ? NC : 1];
@@ -432,14 +614,23 @@ struct Held {
       if constexpr (kHeld == kHeldPacked && V == 8) {
         const uint32_t w = none != 0.f ? 0x3f803f80u : 0u;
         uint4 q = make_uint4(w, w, w, w);
-        if (p && chunk_col<V>(i) < C) q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + chunk_col<V>(i)));
+        const int at = chunk_col<V, NC, kMode>(i);
+        if (p && at + V <= C) {
+          q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
+        } else if (kMode == kShifted && p) {
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[k] = at + k < C ? __ldg(static_cast<const unsigned short*>(p) + at + k) : 0u;
+          q = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        }
         r[i].u[0] = q.x; r[i].u[1] = q.y; r[i].u[2] = q.z; r[i].u[3] = q.w;
       }
     }
   }
   __device__ __forceinline__ Chunk<V> load(int i) const {
     Chunk<V> o;
-    if (p && chunk_col<V>(i) < C) return vec_chunk<V>(p, f32, vec, chunk_col<V>(i), C);
+    const int at = chunk_col<V, NC, kMode>(i);
+    if (p && at < C) return vec_chunk<V>(p, f32, vec, at, C);
 #pragma unroll
     for (int k = 0; k < Chunk<V>::kPairs; ++k) o.p[k] = f2(none, none);
     return o;
@@ -450,30 +641,19 @@ struct Held {
   }
 };
 
-// The span of row j of a turn (V = 1): a padded row lies wholly in its slot.
-template <typename T, int V, int ROWS, int OPS>
-__device__ __forceinline__ RowSpan<T, V> span_of(const Walk<T, V, ROWS, OPS>& walk, int o, int j) {
-  RowSpan<T, V> q(V > 1 ? nullptr : walk.src(o, min(walk.row + j, walk.total() - 1)), walk.p.C);
-  if (V == 1 && walk.row + j >= walk.total()) {
-    q.off = q.lo = 0;
-    q.hi = walk.p.C;
-  }
-  return q;
-}
-
-// Forward, ROWS rows of a CTA per turn (a CTA is one warp where that is enough); NC chunks a thread,
-// all of which exist in every thread when kExact.
-template <typename T, int V, int NC, int ROWS, int kHeld, int kRegs, bool kExact>
+// Forward, ROWS rows of a CTA per turn (a CTA is one warp where that is enough); NC chunks a thread.
+template <typename T, int V, int NC, int ROWS, int kHeld, int kRegs, int kMode>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_fwd_kernel(const NormParams p, const bool layer) {
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[2][16 * ROWS];
   __shared__ uint64_t full[kMaxStages];
   __shared__ int abort_word;
   constexpr int P = Chunk<V>::kPairs;
-  Walk<T, V, ROWS, 1> walk(p, ring_mem, full);
+  Walk<T, kMode, ROWS, 1> walk(p, ring_mem, full);
   walk.begin(&abort_word);
-  const Held<V, NC, kHeld> w(p.w, p.w_f32, p.w_vec, p.C, 1.f), b(p.b, p.b_f32, p.b_vec, p.C, 0.f);
-  auto have = [&](int i) { return kExact || chunk_col<V>(i) < p.C; };
+  const Held<V, NC, kHeld, kMode> w(p.w, p.w_f32, p.w_vec, p.C, 1.f), b(p.b, p.b_f32, p.b_vec, p.C, 0.f);
+  auto col = [&](int i) { return chunk_col<V, NC, kMode>(i); };
+  auto have = [&](int i) { return kMode == kExact || col(i) < p.C; };
   T* y = static_cast<T*>(p.y) + walk.row * p.ldy;
   const long long y_step = walk.step * p.ldy;
   bool fail = false;
@@ -485,14 +665,14 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_fwd_kerne
     float sum[ROWS], mu[ROWS];
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      const RowSpan<T, V> q = span_of(walk, 0, j);
+      const uint32_t at = walk.column0(j, 0);
       F2 t = f2(0.f, 0.f);
       mu[j] = 0.f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         if (have(i)) {
           RawChunk<T, V> r;
-          r.load(walk.at(j, 0), q, chunk_col<V>(i), p.C);
+          r.template load<kMode>(at + static_cast<uint32_t>(col(i)) * static_cast<uint32_t>(sizeof(T)), p.C - col(i));
           x[j][i] = r.values();
         } else {
           x[j][i].zero();
@@ -510,10 +690,14 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_fwd_kerne
         mu[j] = sum[j] * p.inv_c;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-          const F2 nm = f2(have(i) ? -mu[j] : 0.f,
-                           !have(i) || (V == 1 && chunk_col<V>(i) + static_cast<int>(blockDim.x) >= p.C) ? 0.f : -mu[j]);
+          const float m = have(i) ? -mu[j] : 0.f;
+          const F2 nm = f2(m, m);
 #pragma unroll
           for (int k = 0; k < P; ++k) x[j][i].p[k] = f2_add(x[j][i].p[k], nm);
+          if (kMode == kShifted && have(i) && col(i) + V > p.C) {
+            asm volatile("" ::: "memory");   // a branch that few warps take, not selects in all
+            x[j][i].cut(p.C - col(i));
+          }
         }
       }
     }
@@ -528,7 +712,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_fwd_kerne
     }
     cta_sum<ROWS>(sum, red[odd], fail);  // every thread has read the stage; `fail` is now the CTA's
     odd ^= 1;
-    if (!fail) walk.refill();
+    if (kMode != kShifted && !fail) walk.refill();
     const int rows = walk.total() - walk.row;
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
@@ -540,18 +724,27 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_fwd_kerne
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      if (have(i)) {
-        const Chunk<V> wc = w.at(i), bc = b.at(i);
+      if (!have(i)) continue;
+      const Chunk<V> wc = w.at(i), bc = b.at(i);
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) {
-          const F2 rr = f2(sum[j], sum[j]);
+      for (int j = 0; j < ROWS; ++j) {
+        const F2 rr = f2(sum[j], sum[j]);
 #pragma unroll
-          for (int k = 0; k < P; ++k) x[j][i].p[k] = f2_fma(f2_mul(x[j][i].p[k], rr), wc.p[k], bc.p[k]);
-          if (j < rows) store_chunk<T, V>(y + j * p.ldy, x[j][i], chunk_col<V>(i), p.C);
-        }
+        for (int k = 0; k < P; ++k) x[j][i].p[k] = f2_fma(f2_mul(x[j][i].p[k], rr), wc.p[k], bc.p[k]);
+        if (kMode != kShifted && j < rows) store_chunk<T, V>(y + j * p.ldy, x[j][i], col(i));
+      }
+    }
+    if constexpr (kMode == kShifted) {
+      T* yr = y;
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j, yr += p.ldy) {
+        ShiftedStore<T, V, NC, kMode> shifted(yr);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) shifted.put(x[j][i], i, p.C, j < rows && have(i));
       }
     }
     if (fail) break;
+    if (kMode == kShifted) walk.refill();                // here the rows' registers are free
   }
   if (fail) walk.settle();
 }
@@ -606,18 +799,19 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_long_kernel(const NormPa
 // Backward, ROWS rows of a CTA per turn; NC chunks a thread.  Between the sums and dx a thread keeps
 // xh and h of its columns, or (kRaw, where those and dw, db would not fit its registers) the raw
 // elements, and forms them again.
-template <typename T, int V, int NC, int ROWS, bool kRaw, int kHeld, int kRegs, bool kExact>
+template <typename T, int V, int NC, int ROWS, bool kRaw, int kHeld, int kRegs, int kMode>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kernel(const NormParams p, const bool layer) {
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[2][16 * 2 * ROWS];
   __shared__ uint64_t full[kMaxStages];
   __shared__ int abort_word;
   constexpr int P = Chunk<V>::kPairs;
-  Walk<T, V, ROWS, 2> walk(p, ring_mem, full);
+  Walk<T, kMode, ROWS, 2> walk(p, ring_mem, full);
   walk.begin(&abort_word);
   if (threadIdx.x == 0) grid_launch_dependents();     // the column sums' second kernel may take its place
-  auto have = [&](int i) { return kExact || chunk_col<V>(i) < p.C; };
-  const Held<V, NC, kHeld> wh(p.w, p.w_f32, p.w_vec, p.C, 1.f);
+  auto col = [&](int i) { return chunk_col<V, NC, kMode>(i); };
+  auto have = [&](int i) { return kMode == kExact || col(i) < p.C; };
+  const Held<V, NC, kHeld, kMode> wh(p.w, p.w_f32, p.w_vec, p.C, 1.f);
   Chunk<V> dw[NC], db[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
@@ -654,7 +848,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kerne
     float sums[2 * ROWS];
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-      const RowSpan<T, V> qx = span_of(walk, 0, j), qg = span_of(walk, 1, j);
+      const uint32_t ax = walk.column0(j, 0), ag = walk.column0(j, 1);
       const F2 nm = f2(-mu[j], -mu[j]), rr = f2(r[j], r[j]);
       F2 s1 = f2(0.f, 0.f), s2 = f2(0.f, 0.f);
 #pragma unroll
@@ -662,8 +856,9 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kerne
         if (!have(i)) continue;
         const Chunk<V> w = wh.at(i);
         RawChunk<T, V> a, g;
-        a.load(walk.at(j, 0), qx, chunk_col<V>(i), p.C);
-        g.load(walk.at(j, 1), qg, chunk_col<V>(i), p.C);
+        const uint32_t at = static_cast<uint32_t>(col(i)) * static_cast<uint32_t>(sizeof(T));
+        a.template load<kMode>(ax + at, p.C - col(i));
+        g.template load<kMode>(ag + at, p.C - col(i));
         if (kRaw) {
           rx[j][kRaw ? i : 0] = a;
           rg[j][kRaw ? i : 0] = g;
@@ -687,7 +882,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kerne
       sums[2 * j + 1] = f2_sum(s2);
     }
     cta_sum<2 * ROWS>(sums, red[odd], fail);   // every thread has read the stage; `fail` is the CTA's
-    if (!fail) walk.refill();
+    if (kMode != kShifted && !fail) walk.refill();
     if (walk.total() - walk.row > walk.step) stats_of(walk.row + walk.step);
     if (p.y) {
       const int rows = walk.total() - walk.row;
@@ -695,11 +890,15 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kerne
       for (int j = 0; j < ROWS; ++j) {
         const float m1 = layer ? sums[2 * j] * p.inv_c : 0.f, m2 = sums[2 * j + 1] * p.inv_c;
         const F2 a = f2(-m1, -m1), b = f2(-m2, -m2), rr = f2(r[j], r[j]), nm = f2(-mu[j], -mu[j]);
+        ShiftedStore<T, V, NC, kMode> shifted(y + j * p.ldy);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-          if (!have(i)) continue;
+          if (kMode != kShifted && !have(i)) continue;
           Chunk<V> xh, hh;
-          if (kRaw) {
+          if (kMode == kShifted && !have(i)) {
+            xh.zero();
+            hh.zero();
+          } else if (kRaw) {
             xh = rx[j][kRaw ? i : 0].values();
             hh = rg[j][kRaw ? i : 0].values();
             const Chunk<V> w = wh.at(i);
@@ -714,11 +913,13 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kerne
           }
 #pragma unroll
           for (int k = 0; k < P; ++k) xh.p[k] = f2_mul(f2_fma(xh.p[k], b, f2_add(hh.p[k], a)), rr);
-          if (j < rows) store_chunk<T, V>(y + j * p.ldy, xh, chunk_col<V>(i), p.C);
+          if constexpr (kMode == kShifted) shifted.put(xh, i, p.C, j < rows && have(i));
+          else if (j < rows) store_chunk<T, V>(y + j * p.ldy, xh, col(i));
         }
       }
     }
     if (fail) break;
+    if (kMode == kShifted) walk.refill();                // here the rows' registers are free
   }
   if (fail) walk.settle();
   if (!p.part) return;
@@ -726,8 +927,8 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(kRegs) norm_bwd_kerne
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     if (!have(i)) continue;
-    store_sums<V>(out, dw[i], chunk_col<V>(i), p.C);
-    store_sums<V>(out + p.C, db[i], chunk_col<V>(i), p.C);
+    store_sums<V>(out, dw[i], col(i), p.C);
+    store_sums<V>(out + p.C, db[i], col(i), p.C);
   }
 }
 
@@ -852,13 +1053,11 @@ bool ring_form(Form* f, long long C, bool f32, bool vec, int ops) {
 // Forward: 16 or so elements a thread and four rows a turn, so that what a turn costs besides its
 // elements (waits, sums, barriers) is spread over 64; longer rows take more elements and fewer rows.
 Form fwd_form(long long C, bool f32, bool vec) {
-  const long long n = vec ? C / (f32 ? 4 : 8) : C;
+  const long long n = (C + (f32 ? 3 : 7)) / (f32 ? 4 : 8);
   Form f{0, 1, kMaxThreads, 64, 2, 0, 0};
   if (C > (1 << 20)) return f;
-  struct { int nv, rows, top, regs; } const vecs[] = {{1, 4, 64, 104}, {2, 4, 512, 128}, {4, 2, 512, 128}, {8, 1, 512, 128}},
-                                            ones[] = {{2, 4, 64, 64}, {8, 4, 384, 96}, {16, 2, 512, 112}, {32, 1, 512, 96}};
-  for (int i = 0; i < 4; ++i) {
-    const auto& q = vec ? vecs[i] : ones[i];
+  struct { int nv, rows, top, regs; } const forms[] = {{1, 4, 64, 104}, {2, 4, 512, 128}, {4, 2, 512, 128}, {8, 1, 512, 128}};
+  for (const auto& q : forms) {
     if (n <= static_cast<long long>(q.nv) * q.top) {
       f.nv = q.nv;
       f.rows = q.rows;
@@ -874,17 +1073,16 @@ Form fwd_form(long long C, bool f32, bool vec) {
 // Backward: 8 elements a thread and four rows a turn (its dw, db, weight, xh and h take registers
 // each), 16 and two, or 32 and one.
 Form bwd_form(long long C, bool f32, bool vec) {
-  const long long n = vec ? C / (f32 ? 4 : 8) : C;
+  const long long n = (C + (f32 ? 3 : 7)) / (f32 ? 4 : 8);
   Form f{0, 1, kMaxThreads, 64, 2, 0, 0};
   if (C > (1 << 20)) return f;
   struct { int nv, rows, top, regs; } const v8[] = {{1, 4, 512, 128}, {2, 2, 512, 128}, {4, 1, 512, 128}, {4, 1, 512, 128}},
-                                            v4[] = {{2, 4, 512, 128}, {4, 2, 512, 128}, {8, 1, 512, 128}, {8, 1, 512, 128}},
-                                            ones[] = {{2, 4, 256, 112}, {8, 2, 288, 112}, {16, 1, 512, 112}, {28, 1, 512, 128}};
+                                            v4[] = {{2, 4, 512, 128}, {4, 2, 512, 128}, {8, 1, 512, 128}, {8, 1, 512, 128}};
   for (int i = 0; i < 4; ++i) {
-    const auto& q = !vec ? ones[i] : f32 ? v4[i] : v8[i];
+    const auto& q = f32 ? v4[i] : v8[i];
     if (n <= static_cast<long long>(q.nv) * q.top) {
       f.nv = q.nv;
-      f.rows = q.rows;
+      f.rows = vec ? q.rows : (q.rows + 1) / 2;
       f.regs = q.regs;
       f.threads = row_threads(n, q.nv);
       break;
@@ -927,28 +1125,22 @@ int dispatch_fwd(NormParams p, bool vec, bool layer, cudaStream_t st) {
   const int g = blocks_of(p.T, f);
   const bool exact = vec && p.C == f.nv * f.threads * V;
   const bool packed = (!p.w || (!p.w_f32 && p.w_vec)) && (!p.b || (!p.b_f32 && p.b_vec));
+  const int mode = !vec ? kShifted : exact ? kExact : kWhole;
 #define WP_FWD(...) \
-  (exact ? launch(norm_fwd_kernel<T, V, __VA_ARGS__, true>, g, f, smem, p, layer, st) \
-         : launch(norm_fwd_kernel<T, V, __VA_ARGS__, false>, g, f, smem, p, layer, st))
-  if (vec) {
-    switch (f.nv) {
-      case 1: return WP_FWD(1, 4, kHeldValues, 104);
-      case 2:
-        if constexpr (V == 4) return WP_FWD(2, 4, kHeldValues, 112);
-        else return packed ? WP_FWD(2, 4, kHeldPacked, 128) : WP_FWD(2, 4, kHeldNot, 128);
-      case 4:
-        if constexpr (V == 4) return WP_FWD(4, 2, kHeldValues, 128);
-        else return packed ? WP_FWD(4, 2, kHeldPacked, 128) : WP_FWD(4, 2, kHeldNot, 128);
-      default: return WP_FWD(8, 1, kHeldNot, 128);
-    }
+  (mode == kExact ? launch(norm_fwd_kernel<T, V, __VA_ARGS__, kExact>, g, f, smem, p, layer, st) \
+   : mode == kWhole ? launch(norm_fwd_kernel<T, V, __VA_ARGS__, kWhole>, g, f, smem, p, layer, st) \
+                    : launch(norm_fwd_kernel<T, V, __VA_ARGS__, kShifted>, g, f, smem, p, layer, st))
+  switch (f.nv) {
+    case 1: return WP_FWD(1, 4, kHeldValues, 104);
+    case 2:
+      if constexpr (V == 4) return WP_FWD(2, 4, kHeldValues, 112);
+      else return packed ? WP_FWD(2, 4, kHeldPacked, 128) : WP_FWD(2, 4, kHeldNot, 128);
+    case 4:
+      if constexpr (V == 4) return WP_FWD(4, 2, kHeldValues, 128);
+      else return packed ? WP_FWD(4, 2, kHeldPacked, 128) : WP_FWD(4, 2, kHeldNot, 128);
+    default: return WP_FWD(8, 1, kHeldNot, 128);
   }
 #undef WP_FWD
-  switch (f.nv) {                        // two elements a chunk
-    case 2: return launch(norm_fwd_kernel<T, 1, 1, 4, kHeldValues, 64, false>, g, f, smem, p, layer, st);
-    case 8: return launch(norm_fwd_kernel<T, 1, 4, 4, kHeldValues, 96, false>, g, f, smem, p, layer, st);
-    case 16: return launch(norm_fwd_kernel<T, 1, 8, 2, kHeldValues, 112, false>, g, f, smem, p, layer, st);
-    default: return launch(norm_fwd_kernel<T, 1, 16, 1, kHeldNot, 96, false>, g, f, smem, p, layer, st);
-  }
 }
 
 template <typename T>
@@ -965,31 +1157,25 @@ int dispatch_bwd(NormParams p, bool vec, bool layer, int* grid, cudaStream_t st)
   const size_t smem = static_cast<size_t>(f.stages) * f.rows * 2 * f.slot;
   const bool exact = vec && p.C == f.nv * f.threads * V;
   const bool packed = !p.w || (!p.w_f32 && p.w_vec);
-#define WP_BWD(...) \
-  (exact ? launch(norm_bwd_kernel<T, V, __VA_ARGS__, 128, true>, g, f, smem, p, layer, st) \
-         : launch(norm_bwd_kernel<T, V, __VA_ARGS__, 128, false>, g, f, smem, p, layer, st))
-  if (vec) {
-    if constexpr (V == 8) {
-      switch (f.nv) {
-        case 1: return WP_BWD(1, 4, false, kHeldValues);
-        case 2: return packed ? WP_BWD(2, 2, false, kHeldPacked) : WP_BWD(2, 2, false, kHeldNot);
-        default: return packed ? WP_BWD(4, 1, true, kHeldPacked) : WP_BWD(4, 1, true, kHeldNot);
-      }
-    } else {
-      switch (f.nv) {
-        case 2: return WP_BWD(2, 4, false, kHeldValues);
-        case 4: return WP_BWD(4, 2, false, kHeldValues);
-        default: return WP_BWD(8, 1, false, kHeldNot);
-      }
+  const int mode = !vec ? kShifted : exact ? kExact : kWhole;
+#define WP_BWD(NC, ROWS, RAW, HELD)                                                                                 \
+  (mode == kExact   ? launch(norm_bwd_kernel<T, V, NC, ROWS, RAW, HELD, 128, kExact>, g, f, smem, p, layer, st)     \
+   : mode == kWhole ? launch(norm_bwd_kernel<T, V, NC, ROWS, RAW, HELD, 128, kWhole>, g, f, smem, p, layer, st)     \
+                    : launch(norm_bwd_kernel<T, V, NC, (ROWS + 1) / 2, RAW, HELD, 128, kShifted>, g, f, smem, p, layer, st))
+  if constexpr (V == 8) {
+    switch (f.nv) {
+      case 1: return WP_BWD(1, 4, false, kHeldValues);
+      case 2: return packed ? WP_BWD(2, 2, false, kHeldPacked) : WP_BWD(2, 2, false, kHeldNot);
+      default: return packed ? WP_BWD(4, 1, true, kHeldPacked) : WP_BWD(4, 1, true, kHeldNot);
+    }
+  } else {
+    switch (f.nv) {
+      case 2: return WP_BWD(2, 4, false, kHeldValues);
+      case 4: return WP_BWD(4, 2, false, kHeldValues);
+      default: return WP_BWD(8, 1, false, kHeldNot);
     }
   }
 #undef WP_BWD
-  switch (f.nv) {                        // two elements a chunk
-    case 2: return launch(norm_bwd_kernel<T, 1, 1, 4, false, kHeldValues, 112, false>, g, f, smem, p, layer, st);
-    case 8: return launch(norm_bwd_kernel<T, 1, 4, 2, false, kHeldValues, 112, false>, g, f, smem, p, layer, st);
-    case 16: return launch(norm_bwd_kernel<T, 1, 8, 1, false, kHeldValues, 112, false>, g, f, smem, p, layer, st);
-    default: return launch(norm_bwd_kernel<T, 1, 14, 1, false, kHeldNot, 128, false>, g, f, smem, p, layer, st);
-  }
 }
 
 bool valid_rows(const wp_mat* m) {
