@@ -193,3 +193,11 @@ def test_no_rows_other_stream_and_graph():
             torch.cuda.synchronize()
             assert torch.equal(out, w)
     assert wpg.lora_device_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 17, 24, 25, 33, 41, 48, 49, 64, 65, 97, 128, 129, 200, 256])
+@pytest.mark.parametrize("K,N,G,R", [(64, 72, 1, 8), (960, 216, 3, 24), (6464, 40, 1, 16), (512, 5136, 2, 32)])
+def test_rows_over_a_4_bit_weight(K, N, G, R, T):
+    lay = Layer(T, K, N, G, R, 6, base="nf4", bias="bf16", seed=K + T, ldx=K + 8)
+    first = lay.check(_slots(T, 6, "any", K + T), 0.8)
+    assert torch.equal(lay.run(_slots(T, 6, "any", K + T), 0.8), first)

@@ -210,3 +210,29 @@ def test_no_rows_and_other_stream():
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got, want) and torch.equal(st0, st1)
     assert all(torch.equal(a, b) for a, b in zip(grads, wpg.lora_norm_bwd(x, x, None, st0)))
+
+
+def _placed(T, C, ld, off, dtype, seed, shift=0.3):
+    """[T, C] rows ld apart, the first `off` elements past a 256-byte boundary, NaN around them."""
+    buf = torch.full((off + T * ld + 64,), float("nan"), dtype=dtype, device=gu.DEV)
+    x = buf[off:off + T * ld].view(T, ld)[:, :C]
+    x.copy_(_data(T, C, dtype, seed, shift))
+    return x
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,C", [(T, C) for T in (1, 2, 3, 4, 5, 9)
+                                 for C in (1, 2, 3, 5, 8, 9, 31, 63, 255, 263, 511, 1025, 2051, 4095, 8191, 16001)]
+                         + [(1300, C) for C in (1, 3, 8, 31, 255)])
+def test_rows_at_any_place(T, C, dtype):
+    for i, gap in enumerate((0, 0, 5)):              # rows one after another, and apart
+        x = _placed(T, C, C + gap, (0, 3, 6)[i], dtype, 1)
+        dy = _placed(T, C, C + (gap + 3 if gap else 0), (5, 0, 1)[i], dtype, 2, 0.0)
+        w, b = _vec(C + 1, dtype, 3, 1.0)[i % 2:][:C], _vec(C + 2, torch.float32, 4, 0.0)[i:][:C]
+        off, ld = (7, 2, 4)[i], C + (gap and 11)
+        out = torch.full((off + T * ld + 64,), 7.0, dtype=dtype, device=gu.DEV)
+        y, stats = wpg.lora_norm_fwd(x, w, b, 1e-5, out=out[off:off + T * ld].view(T, ld)[:, :C])
+        _check_fwd(x, w, b, wpg.WP_NORM_LAYER, 1e-5, y, stats)
+        y.fill_(7.0)
+        assert bool((out == 7.0).all())
+        _check_bwd(dy, x, w, wpg.WP_NORM_LAYER, stats)

@@ -338,7 +338,7 @@ int record_cuda() {
 // WP_ERR_UNSUPPORTED (before any CUDA call) when the shapes or alignments do not suit it.
 int skinny_impl(const wp_mat* X, const wp_mat* W, const wp_mat* bias, int G, bool grouped,
                 const wp_adapter* adapters, int n_adapters, const float* s_of, const wp_out* Y,
-                void* workspace, cudaStream_t stream, const MultiCall* multi = nullptr) {
+                void* workspace, cudaStream_t stream) {
   SkinnyPlan sp;
   if (!plan_skinny(X, W, adapters, n_adapters, &sp)) return WP_ERR_UNSUPPORTED;
   const long long T = X->rows, K = X->cols, N = sp.N;
@@ -349,13 +349,6 @@ int skinny_impl(const wp_mat* X, const wp_mat* W, const wp_mat* bias, int G, boo
     if (!aligned16(adapters[i].A.data) || adapters[i].A.ld % 8) return WP_ERR_UNSUPPORTED;
   const bool nf4 = W && W->dtype == WP_NF4;
   float* part = static_cast<float*>(workspace);
-  // rows of many adapters: their H~ is formed by a kernel of its own, beside the weight's
-  const bool early = multi != nullptr;
-  auto begin = [&]() { return multi ? launch_multi_shrink_small(*multi, stream) : WP_OK; };
-  auto finish = [&](const SkinnyReduceParams& r) {
-    return multi ? launch_multi_reduce(r, *multi, stream) : launch_skinny_reduce(r, stream);
-  };
-
   SkinnyReduceParams q{};
   q.T = static_cast<int>(T); q.N = static_cast<int>(N); q.out_g = static_cast<int>(out_g);
   q.R16 = sp.R16; q.splits = sp.splits; q.has_w = W ? 1 : 0;
@@ -401,11 +394,10 @@ int skinny_impl(const wp_mat* X, const wp_mat* W, const wp_mat* bias, int G, boo
     if (!g.status) return record_cuda();
     int rc = WP_OK;
     if (sp.g_ld) {
-      rc = begin();
-      if (rc == WP_OK) rc = launch_gemv_ld(g, W->data, W->absmax, sp.g_grid, stream, early);
+      rc = launch_gemv_ld(g, W->data, W->absmax, sp.g_grid, stream);
       if (rc != WP_OK) return rc;
       q.splits = sp.g_splits;
-      return finish(q);
+      return launch_skinny_reduce(q, stream);
     }
     GemvMaps gm;
     std::memset(&gm, 0, sizeof(gm));
@@ -417,11 +409,10 @@ int skinny_impl(const wp_mat* X, const wp_mat* W, const wp_mat* bias, int G, boo
       rc = make_map_bf16(&gm.w, W->data, K, N, W->ld, kBK, 32);
     }
     if (rc != WP_OK) return rc;
-    rc = begin();
-    if (rc == WP_OK) rc = launch_gemv(gm, g, nf4, sp.g_grid, sp.g_smem, stream, early);
+    rc = launch_gemv(gm, g, nf4, sp.g_grid, sp.g_smem, stream);
     if (rc != WP_OK) return rc;
     q.splits = sp.g_splits;
-    return finish(q);
+    return launch_skinny_reduce(q, stream);
   }
 
   SkinnyMaps maps;
@@ -484,10 +475,9 @@ int skinny_impl(const wp_mat* X, const wp_mat* W, const wp_mat* bias, int G, boo
     rc = make_map_bf16(&maps.a[i], adapters[i].A.data, K, adapters[i].A.rows, adapters[i].A.ld, kBK, 16);
     if (rc != WP_OK) return rc;
   }
-  rc = begin();
-  if (rc == WP_OK) rc = launch_skinny(maps, p, smem, nf4, stream, early);
+  rc = launch_skinny(maps, p, smem, nf4, stream);
   if (rc != WP_OK) return rc;
-  return finish(q);
+  return launch_skinny_reduce(q, stream);
 }
 
 // h_out (optional): s * X A^T of the tensor-core adapters in fp32, [T, h_out_ld], adapters in
@@ -919,16 +909,6 @@ int fwd_impl(const wp_mat* X, const wp_mat* W, const wp_mat* bias, int G, bool g
 }
 
 }  // namespace
-
-int multi_skinny(const MultiCall& c, const wp_mat* X, const wp_mat* W, const wp_mat* bias, const wp_out* Y, void* part,
-                 cudaStream_t stream) {
-  return skinny_impl(X, W, bias, 1, false, nullptr, 0, nullptr, Y, part, stream, &c);
-}
-
-size_t multi_skinny_bytes(const wp_mat* X, const wp_mat* W) {
-  SkinnyPlan sp;
-  return plan_skinny(X, W, nullptr, 0, &sp) ? sp.part_bytes : 0;
-}
 
 // The fused forward over rows of many adapters: the blocks' entries and H~ are already written (or
 // being written by the kernel launched just before).  Arguments are validated by the caller.

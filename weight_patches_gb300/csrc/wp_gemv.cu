@@ -255,7 +255,6 @@ __global__ void __launch_bounds__(kGemvWarps * 32) gemv_kernel(const __grid_cons
       for (int t = 0; t < kT; ++t) part[static_cast<long long>(t) * p.ldp + p.N + ar] = sum[t];
     }
   }
-  grid_dependency_wait();   // started early beside another kernel: this one ends after it
 }
 
 // A 16-byte load of weight bytes read once: not kept in L1.
@@ -410,31 +409,15 @@ __global__ void __launch_bounds__(kGemvLdWarps * 32, 2) gemv_nf4_ld_kernel(const
       if (lane == 0) part[static_cast<long long>(t) * p.ldp + p.N + ar] = sum[t];
     }
   }
-  grid_dependency_wait();   // started early beside another kernel: this one ends after it
-}
-
-// early: as a programmatic dependent of the kernel before (which the kernel waits for at its end)
-template <typename K, typename... Args>
-cudaError_t launch_early(K kern, int grid, int threads, size_t smem, cudaStream_t stream, bool early, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = early ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int kT, bool kNF4>
-int launch_t(const GemvMaps& maps, const GemvParams& p, int grid, size_t smem, cudaStream_t stream, bool early) {
+int launch_t(const GemvMaps& maps, const GemvParams& p, int grid, size_t smem, cudaStream_t stream) {
   auto kern = gemv_kernel<kT, kNF4>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e == cudaSuccess) {
-    e = launch_early(kern, grid, kGemvWarps * 32, smem, stream, early, maps, p);
+    kern<<<grid, kGemvWarps * 32, smem, stream>>>(maps, p);
+    e = cudaGetLastError();
   }
   if (e != cudaSuccess) {
     set_last_cuda_error(e);
@@ -488,12 +471,12 @@ int gemv_blocks_per_sm(int T, bool nf4, size_t smem) {
   return n;
 }
 
-int launch_gemv_ld(const GemvParams& p, const void* codes, const float* absmax, int grid, cudaStream_t stream,
-                   bool early) {
+int launch_gemv_ld(const GemvParams& p, const void* codes, const float* absmax, int grid, cudaStream_t stream) {
   if (grid < 1) return WP_OK;
   const uint8_t* c = static_cast<const uint8_t*>(codes);
   if (p.T != 1) return WP_ERR_UNSUPPORTED;
-  const cudaError_t e = launch_early(gemv_nf4_ld_kernel<1>, grid, kGemvLdWarps * 32, 0, stream, early, p, c, absmax);
+  gemv_nf4_ld_kernel<1><<<grid, kGemvLdWarps * 32, 0, stream>>>(p, c, absmax);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_last_cuda_error(e);
     return WP_ERR_CUDA;
@@ -502,22 +485,22 @@ int launch_gemv_ld(const GemvParams& p, const void* codes, const float* absmax, 
 }
 
 int launch_gemv(const GemvMaps& maps, const GemvParams& p, bool nf4, int grid, size_t smem,
-                cudaStream_t stream, bool early) {
+                cudaStream_t stream) {
   if (grid < 1) return WP_OK;
   if (nf4) {
     switch (p.T) {
-      case 1: return launch_t<1, true>(maps, p, grid, smem, stream, early);
-      case 2: return launch_t<2, true>(maps, p, grid, smem, stream, early);
-      case 3: return launch_t<3, true>(maps, p, grid, smem, stream, early);
-      case 4: return launch_t<4, true>(maps, p, grid, smem, stream, early);
+      case 1: return launch_t<1, true>(maps, p, grid, smem, stream);
+      case 2: return launch_t<2, true>(maps, p, grid, smem, stream);
+      case 3: return launch_t<3, true>(maps, p, grid, smem, stream);
+      case 4: return launch_t<4, true>(maps, p, grid, smem, stream);
       default: return WP_ERR_UNSUPPORTED;
     }
   }
   switch (p.T) {
-    case 1: return launch_t<1, false>(maps, p, grid, smem, stream, early);
-    case 2: return launch_t<2, false>(maps, p, grid, smem, stream, early);
-    case 3: return launch_t<3, false>(maps, p, grid, smem, stream, early);
-    case 4: return launch_t<4, false>(maps, p, grid, smem, stream, early);
+    case 1: return launch_t<1, false>(maps, p, grid, smem, stream);
+    case 2: return launch_t<2, false>(maps, p, grid, smem, stream);
+    case 3: return launch_t<3, false>(maps, p, grid, smem, stream);
+    case 4: return launch_t<4, false>(maps, p, grid, smem, stream);
     default: return WP_ERR_UNSUPPORTED;
   }
 }

@@ -227,10 +227,8 @@ struct SkinnyReduceParams {
   int y_f32;
 };
 
-// early: launched as a programmatic dependent of the kernel before it, whose results it does not
-// read; it ends after that kernel has
 int launch_skinny(const SkinnyMaps& maps, const SkinnyParams& p, size_t smem_bytes, bool nf4,
-                  cudaStream_t stream, bool early);
+                  cudaStream_t stream);
 int launch_skinny_reduce(const SkinnyReduceParams& q, cudaStream_t stream);
 int skinny_grid_ctas(size_t smem_bytes, bool nf4);
 
@@ -280,9 +278,8 @@ struct GemvMaps {
 size_t gemv_smem_bytes(int T, int ks_len);
 int gemv_blocks_per_sm(int T, bool nf4, size_t smem_bytes);
 int launch_gemv(const GemvMaps& maps, const GemvParams& p, bool nf4, int grid, size_t smem_bytes,
-                cudaStream_t stream, bool early);
-int launch_gemv_ld(const GemvParams& p, const void* codes, const float* absmax, int grid, cudaStream_t stream,
-                   bool early);
+                cudaStream_t stream);
+int launch_gemv_ld(const GemvParams& p, const void* codes, const float* absmax, int grid, cudaStream_t stream);
 int* tc_status_ptr();
 
 int tc_max_pairs(size_t smem_bytes, bool nf4);
@@ -545,13 +542,11 @@ int multi_fused(const MultiCall& c, const wp_mat* W, cudaStream_t stream);   // 
 // rows as the MMA's width, K split over a cluster.
 int launch_multi_shrink_small(const MultiCall& c, cudaStream_t stream);
 int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStream_t stream);
-// A few rows against a 4-bit weight: H~ as above, the small-token kernels' partial sums
-// (wp_skinny.cu, wp_gemv.cu) and a reduction of its own.  WP_ERR_UNSUPPORTED, before anything is
-// launched, where their shapes or alignments do not suit.
-int launch_multi_reduce(const SkinnyReduceParams& q, const MultiCall& c, cudaStream_t stream);
-int multi_skinny(const MultiCall& c, const wp_mat* X, const wp_mat* W, const wp_mat* bias, const wp_out* Y, void* part,
-                 cudaStream_t stream);                                              // wp_api.cu
-size_t multi_skinny_bytes(const wp_mat* X, const wp_mat* W);
+// A few rows against a 4-bit weight (wp_multi_nf4.cu): H~ as above, partial sums over parts of K (0 parts:
+// K is too long), and their sum with the adapters' term.
+int multi_nf4_parts(int T, int N, int K);
+int launch_multi_nf4(const MultiCall& c, const void* codes, const float* absmax, float* part, int parts,
+                     cudaStream_t stream);
 
 int encode_map_bf16(CUtensorMap* m, const void* ptr, long long inner, long long outer, long long ld, int box_inner,
                     int box_outer, int swizzle);

@@ -5,8 +5,8 @@
 // (sglang PR, Motivation: the adapter and its scale belong to the request, so a batch meets
 // many of them.)  The adapters of a layer lie in a bank, one per slot, and every row names its
 // slot on the device.  This file holds the entry point: its checks, its workspace and the choice
-// between the forms -- a few rows, where the weights' bytes are the work (wp_multi_small.cu; with a
-// 4-bit weight the small-token kernels of wp_skinny.cu and wp_gemv.cu), and many (the blocks' slots and H~ in wp_multi_shrink.cu, then the fused forward of wp_tc_fwd.cu
+// between the forms -- a few rows, where the weights' bytes are the work (wp_multi_small.cu; a 4-bit
+// weight in wp_multi_nf4.cu), and many (the blocks' slots and H~ in wp_multi_shrink.cu, then the fused forward of wp_tc_fwd.cu
 // with a lane mask per slot).
 #include <cmath>
 
@@ -50,8 +50,14 @@ int check(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
 // 27-60 us on five layers (1536 -> 4608 and 8960, 4096^2, 5120^2, 8960 -> 1536; 8-16 slots in any order, in runs
 // or one) where the masked fused forward took 28-111; at 512 rows of one slot 28-69 against 29-66.
 constexpr int kSmallRows = 256;
-// Rows up to which a 4-bit weight takes the small-token kernels.
-bool nf4_few(int T, const wp_mat* W) { return T <= kSkinnyMaxT && W && W->dtype == WP_NF4; }
+// Rows up to which a 4-bit weight takes the kernels that decode it into fragments: they decode it once per
+// 64 rows, the fused forward once per 512.  At 128 rows they took 24-140 us on nine layers (N 1536 to 28672,
+// K 1536 to 14336) where the fused forward took 44-176 and in no case 6% more; at 256 rows
+// 35-135 against 45-177 on the five with N <= 5120, too few column tiles to fill the fused forward's SMs,
+// but 60-287 against 45-142 on the others.
+bool nf4_few(long long T, const wp_mat* W) {
+  return W && W->dtype == WP_NF4 && (T <= 128 || (T <= 256 && W->rows <= 5120));
+}
 bool small_rows(int T, const wp_mat* W) { return T <= kSmallRows && (!W || W->dtype == WP_BF16); }
 
 // H~ [T, G R16] | act [T] (few rows), or s [T] | entries | their counts | rows with an adapter
@@ -59,6 +65,7 @@ bool small_rows(int T, const wp_mat* W) { return T <= kSmallRows && (!W || W->dt
 struct Layout {
   size_t act = 0, ent = 0, ent_n = 0, ent_rows = 0, part = 0, total = 0;
   int ent_ld = 0;
+  int parts = 0;                          // of K, few rows over a 4-bit weight
 };
 
 Layout layout(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
@@ -72,7 +79,10 @@ Layout layout(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
     L.ent_n = L.ent + r256(blocks * L.ent_ld * sizeof(MultiEntry));
     L.ent_rows = L.ent_n + r256(blocks * 4);
     L.total = L.part = L.ent_rows + r256(blocks * 32);
-    if (nf4_few(static_cast<int>(T), W)) L.total += multi_skinny_bytes(X, W);
+    if (nf4_few(X->rows, W)) {
+      L.parts = multi_nf4_parts(static_cast<int>(T), static_cast<int>(bank->out), static_cast<int>(bank->in));
+      L.total += static_cast<size_t>(L.parts) * T * bank->out * 4;
+    }
   }
   return L;
 }
@@ -140,9 +150,10 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
     if (rc != WP_OK) return rc;
     return launch_multi_small(c, W ? W->data : nullptr, W ? W->ld : 0, st);
   }
-  if (nf4_few(c.T, W)) {
-    rc = multi_skinny(c, X, W, bias, Y, ws + L.part, st);
-    if (rc != WP_ERR_UNSUPPORTED) return rc;
+  if (L.parts) {
+    rc = launch_multi_shrink_small(c, st);
+    if (rc != WP_OK) return rc;
+    return launch_multi_nf4(c, W->data, W->absmax, reinterpret_cast<float*>(ws + L.part), L.parts, st);
   }
   c.srow = reinterpret_cast<float*>(ws + L.act);
   c.ent = reinterpret_cast<MultiEntry*>(ws + L.ent);

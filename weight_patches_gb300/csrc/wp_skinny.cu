@@ -405,7 +405,6 @@ __global__ void __launch_bounds__(kNF4 ? kSkinnyThreadsNF4 : kSkinnyThreads, 1)
   // after an abort: the last copy into each code slot may still be in flight
   if (kNF4 && threadIdx.x == 0 && *abort_flag)
     for (int c = 0; c < R; ++c) settle(&code_full[c], c_uses[c]);
-  grid_dependency_wait();   // started early beside another kernel: this one ends after it
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 128);
@@ -543,91 +542,13 @@ __global__ void __launch_bounds__(256) skinny_reduce_kernel(const SkinnyReducePa
   }
 }
 
-// Rows of many adapters: the K splits' sums, the bias and each row's own H~ B_a^T (H~ and the rows'
-// slots come from the kernel launched before the weight's), one rounding.  A thread finishes one
-// output column of up to kNT rows; its B rows are read 8 ranks at a time, four rows' loads in flight.
-template <int kNT>
-__global__ void __launch_bounds__(256) multi_reduce_kernel(const SkinnyReduceParams q, const MultiCall c) {
-  const int t0 = blockIdx.y * kNT;
-  const int nt = min(kNT, q.T - t0);
-  const int n = blockIdx.x * blockDim.x + threadIdx.x;
-  if (n >= q.N) return;
-  float bias = 0.f;
-  if (q.bias)
-    bias = q.bias_f32 ? static_cast<const float*>(q.bias)[n]
-                      : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(q.bias)[n]) << 16);
-  grid_dependency_wait();
-  const uint16_t* Hg = c.H + static_cast<long long>(t0) * c.G * c.R16 + n / c.og * c.R16;
-  const int hld = c.G * c.R16;
-  float d[kNT];
-  constexpr int U = kNT < 4 ? kNT : 4;
-#pragma unroll
-  for (int i0 = 0; i0 < kNT; i0 += U) {
-    const uint16_t* b[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int a = i0 + u < nt ? c.act[t0 + i0 + u] : -1;
-      b[u] = a >= 0 ? c.B + (static_cast<long long>(a) * q.N + n) * c.R : nullptr;
-      d[i0 + u] = 0.f;
-    }
-    for (int r = 0; r < c.R; r += 8) {
-      uint4 bv[U], hv[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        bv[u] = hv[u] = make_uint4(0, 0, 0, 0);
-        if (b[u]) {
-          bv[u] = __ldg(reinterpret_cast<const uint4*>(b[u] + r));
-          hv[u] = *reinterpret_cast<const uint4*>(Hg + (i0 + u) * hld + r);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint32_t bw[4] = {bv[u].x, bv[u].y, bv[u].z, bv[u].w};
-        const uint32_t hw[4] = {hv[u].x, hv[u].y, hv[u].z, hv[u].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          d[i0 + u] = fmaf(__uint_as_float(hw[k] << 16), __uint_as_float(bw[k] << 16), d[i0 + u]);
-          d[i0 + u] = fmaf(__uint_as_float(hw[k] & 0xffff0000u), __uint_as_float(bw[k] & 0xffff0000u), d[i0 + u]);
-        }
-      }
-    }
-  }
-  float acc[kNT];
-#pragma unroll
-  for (int t = 0; t < kNT; ++t) acc[t] = 0.f;
-  sum_splits_t<kNT>(q.part + static_cast<long long>(t0) * q.ldp + n, static_cast<long long>(q.T) * q.ldp, q.ldp,
-                    q.splits, nt, acc);
-#pragma unroll
-  for (int t = 0; t < kNT; ++t) {
-    if (t >= nt) break;
-    const float y = (acc[t] + bias) + d[t];
-    const long long o = static_cast<long long>(t0 + t) * q.ldy + n;
-    if (q.y_f32) {
-      static_cast<float*>(q.Y)[o] = y;
-    } else {
-      uint16_t yb;
-      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(yb) : "f"(y));
-      static_cast<uint16_t*>(q.Y)[o] = yb;
-    }
-  }
-}
-
 template <bool kNF4>
-int launch_impl(const SkinnyMaps& maps, const SkinnyParams& p, int grid, size_t smem, cudaStream_t stream, bool early) {
+int launch_impl(const SkinnyMaps& maps, const SkinnyParams& p, int grid, size_t smem, cudaStream_t stream) {
   auto kern = skinny_kernel<kNF4>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kNF4 ? kSkinnyThreadsNF4 : kSkinnyThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = early ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kern, maps, p);
+    kern<<<grid, kNF4 ? kSkinnyThreadsNF4 : kSkinnyThreads, smem, stream>>>(maps, p);
+    e = cudaGetLastError();
   }
   if (e != cudaSuccess) {
     set_last_cuda_error(e);
@@ -648,36 +569,12 @@ int skinny_grid_ctas(size_t smem_bytes, bool nf4) {
 }
 
 int launch_skinny(const SkinnyMaps& maps, const SkinnyParams& p, size_t smem_bytes, bool nf4,
-                  cudaStream_t stream, bool early) {
+                  cudaStream_t stream) {
   int grid = device_sm_count();
   if (grid > p.units) grid = p.units;
   if (grid < 1) return WP_OK;
-  return nf4 ? launch_impl<true>(maps, p, grid, smem_bytes, stream, early)
-             : launch_impl<false>(maps, p, grid, smem_bytes, stream, early);
-}
-
-int launch_multi_reduce(const SkinnyReduceParams& q, const MultiCall& c, cudaStream_t stream) {
-  const int nt = q.T <= 4 ? q.T : 8;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((q.N + 255) / 256, (q.T + nt - 1) / nt);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e;
-  switch (nt) {
-    case 1: e = cudaLaunchKernelEx(&cfg, multi_reduce_kernel<1>, q, c); break;
-    case 2: e = cudaLaunchKernelEx(&cfg, multi_reduce_kernel<2>, q, c); break;
-    case 3: e = cudaLaunchKernelEx(&cfg, multi_reduce_kernel<3>, q, c); break;
-    case 4: e = cudaLaunchKernelEx(&cfg, multi_reduce_kernel<4>, q, c); break;
-    default: e = cudaLaunchKernelEx(&cfg, multi_reduce_kernel<8>, q, c); break;
-  }
-  if (e == cudaSuccess) return WP_OK;
-  set_last_cuda_error(e);
-  return WP_ERR_CUDA;
+  return nf4 ? launch_impl<true>(maps, p, grid, smem_bytes, stream)
+             : launch_impl<false>(maps, p, grid, smem_bytes, stream);
 }
 
 int launch_skinny_reduce(const SkinnyReduceParams& q, cudaStream_t stream) {
