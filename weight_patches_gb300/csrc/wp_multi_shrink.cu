@@ -14,6 +14,7 @@
 // the MMAs, warps 2..5 the output.
 // K is split over a cluster when the blocks do not fill the SMs; the partial sums meet in
 // distributed shared memory and are added in CTA order.
+#include <algorithm>
 #include <atomic>
 
 #include <cuda.h>
@@ -106,6 +107,7 @@ struct ShrinkParams {
   int nc;                      // rank rows per CTA (a multiple of 16, at most 128)
   int splits, kb_per, k_blocks;
   int a_area;                  // bytes of the A ring
+  int shares;                  // CTAs (blockIdx.z) that share a block's slots
 };
 constexpr uint32_t kTmemCols = 256;           // two CTAs per SM
 
@@ -122,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ int e_slot[128];
   __shared__ __align__(16) uint32_t e_off[128][4];      // read and written 16 bytes at a time
   __shared__ __align__(16) uint32_t g_off[128][4];      // the groups': the lanes that none of its slots owns
+  __shared__ __align__(16) uint32_t all_off[4];         // the lanes that no slot of this CTA owns
   __shared__ int e_n;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -181,8 +184,32 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       kept += __popc(b);
     }
-    if (lane == 0) e_n = kept;
     __syncwarp();
+    if (p.shares > 1) {                            // this CTA's share of the slots: whole groups, moved to the front
+      const int cap = max(1, min(min(256 / p.nc, p.a_area / (2 * p.nc * 128)), kept));
+      const int groups = (kept + cap - 1) / cap, z = static_cast<int>(blockIdx.z);
+      const int e0 = z * groups / p.shares * cap, e1 = min(kept, (z + 1) * groups / p.shares * cap);
+      kept = max(0, e1 - e0);
+      for (int i0 = 0; i0 < kept && e0 > 0; i0 += 32) {
+        const int i = min(i0 + lane, kept - 1);
+        const int slot = e_slot[e0 + i];
+        const uint4 m = *reinterpret_cast<const uint4*>(e_off[e0 + i]);
+        __syncwarp();
+        e_slot[i] = slot;
+        *reinterpret_cast<uint4*>(e_off[i]) = m;
+        __syncwarp();
+      }
+    }
+    // the rows of these slots
+    uint4 own = make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (int e = 0; e < kept; ++e) {
+      const uint4 q = *reinterpret_cast<const uint4*>(e_off[e]);
+      own.x &= q.x; own.y &= q.y; own.z &= q.z; own.w &= q.w;
+    }
+    if (lane == 0) {
+      e_n = kept;
+      *reinterpret_cast<uint4*>(all_off) = own;
+    }
     const int gs = max(1, min(min(256 / p.nc, p.a_area / (2 * p.nc * 128)), kept));
     for (int g = lane; g * gs < kept; g += 32) {
       uint4 m = make_uint4(~0u, ~0u, ~0u, ~0u);
@@ -326,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = threadIdx.x; i < share * units && ne > 0; i += kThreads) {
       const int row = rank * share + i / units, u = i % units;
       const int t = t0 + row, j = j0 + u * 8;
-      if (t >= c.T || j >= rows) continue;
+      if (t >= c.T || j >= rows || ((all_off[row >> 5] >> (row & 31)) & 1u)) continue;
       float4 a[8][2];                                  // every split's loads before the first sum
       const uint32_t at = smem_u32(part + row * (p.nc + 4) + u * 8);
 #pragma unroll
@@ -397,7 +424,16 @@ int launch_multi_shrink(const MultiCall& c, cudaStream_t stream) {
   while (p.splits < 8 && 2ll * p.splits * blocks * chunks <= 2ll * device_sm_count() && p.k_blocks >= 4 * p.splits)
     p.splits *= 2;
   p.kb_per = (p.k_blocks + p.splits - 1) / p.splits;
-  p.a_area = (kSmem - 1024 - kXStages * kATileBytes) / 1024 * 1024;
+  // Where that leaves SMs idle, the slots a block can hold are shared out as well (X is then read by each
+  // share, from L2), up to one and a half CTAs per SM: 777 rows in any order of 12 slots of rank 64 took
+  // 19 us with one share, 14 with four, the whole call 56 and 52; 300 rows of 64 such slots 189 and
+  // 96.  Rows of one slot, whose other shares find nothing, lose a microsecond.  At two CTAs
+  // per SM 1500 rows took 3 to 4 us more than with one share.
+  const int a_area = (kSmem - 1024 - kXStages * kATileBytes) / 1024 * 1024;
+  const int cap = std::max(1, std::min(256 / p.nc, a_area / (2 * p.nc * 128)));
+  const int most = (std::min(c.S, 128) + cap - 1) / cap;
+  p.shares = std::max(1, std::min(most, 3 * device_sm_count() / 2 / (blocks * p.splits * chunks)));
+  p.a_area = a_area;
   const size_t smem = 1024 + kXStages * kATileBytes + static_cast<size_t>(p.a_area);
   // the partial sums [128][nc + 4] lie over the rings (nc <= 128: 66 KiB of 107)
   ShrinkMaps maps{};
@@ -406,7 +442,7 @@ int launch_multi_shrink(const MultiCall& c, cudaStream_t stream) {
     rc = encode_map_bf16(&maps.a, c.A, c.K, static_cast<long long>(c.S) * c.G * c.R, c.K, kBK, p.nc, 128);
   if (rc != WP_OK) return rc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks * p.splits, chunks);
+  cfg.gridDim = dim3(blocks * p.splits, chunks, p.shares);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
