@@ -22,7 +22,7 @@
 //                       rows are there and 5 us for the second kernel; between them 5.9 TB/s)
 //   8000 x 5120 fp32    forward 56 us, 5.9 TB/s; backward 83 us, 5.9 TB/s
 //   16 x 5120 bf16      forward 3.5 us, of which a launch is most
-//   20000 x 2187 bf16   forward 70 us, 2.5 TB/s; backward 161 us, 1.6 TB/s: the shifts, twice the
+//   20000 x 2187 bf16   forward 70 us, 2.5 TB/s; backward 116 us, 2.3 TB/s: the shifts, twice the
 //                       arithmetic of an aligned row, are what bounds these
 //   8000 x 4099 fp32    forward 93 us, 2.8 TB/s; backward 124 us, 3.2 TB/s
 // Shifted rows were read and written element by element first: 96 and 278 us, 102 and 161 us.  Their
@@ -1071,7 +1071,9 @@ Form fwd_form(long long C, bool f32, bool vec) {
 }
 
 // Backward: 8 elements a thread and four rows a turn (its dw, db, weight, xh and h take registers
-// each), 16 and two, or 32 and one.
+// each), 16 and two, or 32 and one.  Shifted rows take half as many rows a turn, and 8 elements a thread
+// only up to 256 threads, so that two CTAs fit an SM: 2187 columns of bf16 took 161 us with 288 threads
+// of 8 elements and 116 with 160 of 16, 2801 columns 164 and 148 (20000 rows).
 Form bwd_form(long long C, bool f32, bool vec) {
   const long long n = (C + (f32 ? 3 : 7)) / (f32 ? 4 : 8);
   Form f{0, 1, kMaxThreads, 64, 2, 0, 0};
@@ -1080,7 +1082,7 @@ Form bwd_form(long long C, bool f32, bool vec) {
                                             v4[] = {{2, 4, 512, 128}, {4, 2, 512, 128}, {8, 1, 512, 128}, {8, 1, 512, 128}};
   for (int i = 0; i < 4; ++i) {
     const auto& q = f32 ? v4[i] : v8[i];
-    if (n <= static_cast<long long>(q.nv) * q.top) {
+    if (n <= static_cast<long long>(q.nv) * (!vec && q.rows == 4 ? 256 : q.top)) {
       f.nv = q.nv;
       f.rows = vec ? q.rows : (q.rows + 1) / 2;
       f.regs = q.regs;
