@@ -1033,13 +1033,15 @@ int row_threads(long long vectors, int nv) {
   return static_cast<int>(((vectors + nv - 1) / nv + 31) / 32 * 32);
 }
 
-// The ring of a form: as many CTAs per SM as its registers allow (at most 16), the
-// stages that then fit their shared memory, at most kMaxStages; fewer CTAs when two stages do not.
+// The ring of a form: as many CTAs per SM as its registers allow (each of the four schedulers has 16384,
+// so 104 and 112 a thread allow no more warps than 128; at most 16 CTAs), the stages that then fit
+// their shared memory, at most kMaxStages; fewer CTAs when two stages do not.  A CTA too many would
+// run after the others, with none beside it.
 bool ring_form(Form* f, long long C, bool f32, bool vec, int ops) {
   const int size = f32 ? 4 : 2;
   f->slot = static_cast<int>((C * size + 15) / 16 * 16 + (vec ? 0 : 16));
   const size_t stage = static_cast<size_t>(f->rows) * ops * f->slot;
-  f->per_sm = 65536 / (f->threads * f->regs);
+  f->per_sm = 16384 / (32 * f->regs) * 4 / (f->threads / 32);
   if (f->per_sm > 16) f->per_sm = 16;
   if (f->per_sm < 1) f->per_sm = 1;
   for (;; --f->per_sm) {
