@@ -201,3 +201,15 @@ def test_rows_over_a_4_bit_weight(K, N, G, R, T):
     lay = Layer(T, K, N, G, R, 6, base="nf4", bias="bf16", seed=K + T, ldx=K + 8)
     first = lay.check(_slots(T, 6, "any", K + T), 0.8)
     assert torch.equal(lay.run(_slots(T, 6, "any", K + T), 0.8), first)
+
+
+@pytest.mark.parametrize("T", [1, 2])
+@pytest.mark.parametrize("base", ["bf16", None])
+@pytest.mark.parametrize("K,N,G,R", [(72, 128, 1, 64), (2048, 384, 3, 32), (1000, 216, 3, 8), (5120, 1152, 2, 64),
+                                     (1536, 80, 5, 8), (328, 1000, 1, 24)])
+def test_one_or_two_rows(K, N, G, R, base, T):
+    lay = Layer(T, K, N, G, R, 4, base=base, bias="fp32", seed=K + R, ldx=K + 8)
+    for slot in ([3, 0], [1, 1], [-1, 2], [2, 9], [-1, -1]):
+        y = lay.check(slot[:T], 0.6)
+        assert torch.equal(lay.run(slot[:T], 0.6), y)
+    lay.check([0, 2][:T], 1.0, row_scale=False, out_dtype=torch.float32)

@@ -540,6 +540,7 @@ int launch_multi_shrink(const MultiCall& c, cudaStream_t stream);
 int multi_fused(const MultiCall& c, const wp_mat* W, cudaStream_t stream);   // wp_api.cu
 // Few rows (wp_multi_small.cu): H~ a (slot, 16 rank rows) per CTA, then W streamed once with the
 // rows as the MMA's width, K split over a cluster.
+bool multi_whole(const MultiCall& c);      // so few rows that the second kernel forms H~, too: no first one
 int launch_multi_shrink_small(const MultiCall& c, cudaStream_t stream);
 int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStream_t stream);
 // A few rows against a 4-bit weight (wp_multi_nf4.cu): H~ as above, partial sums over parts of K (0 parts:

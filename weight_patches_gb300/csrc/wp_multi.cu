@@ -146,7 +146,7 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
   }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (small_rows(c.T, W)) {
-    rc = launch_multi_shrink_small(c, st);
+    if (!multi_whole(c)) rc = launch_multi_shrink_small(c, st);
     if (rc != WP_OK) return rc;
     return launch_multi_small(c, W ? W->data : nullptr, W ? W->ld : 0, st);
   }

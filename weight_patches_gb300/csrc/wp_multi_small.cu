@@ -11,12 +11,14 @@
 //           the slot's rows of X the 8-wide one, both through the same permutation of k so that
 //           every lane loads 16 consecutive bytes -- and leave H~ = bf16(s X A^T).  mma.sync
 //           rather than tcgen05: there is no tile to keep, a row belongs to one slot only.
+//           (One or two rows of few ranks do without: the main kernel forms their H~ from its part of K.)
 //   main    W^T tiles of 128 output columns as the M = 128 operand of tcgen05.mma and the rows of
 //           X (rounded up to 16) as its width, W and X by TMA.  K is split over a cluster of up to
 //           8 CTAs so that every SM is streaming W from the first moment; while they do, eight more
 //           warps form the adapters' term of the CTA's share of the rows, 16 output columns a warp,
 //           rows of one slot together up to 8 (the mma.sync fragments again, straight from global
 //           memory), and the partial tiles meet through distributed shared memory, added in CTA order.
+#include <algorithm>
 #include <atomic>
 
 #include <cuda.h>
@@ -181,6 +183,7 @@ constexpr int kSmallMaxStages = 8;
 struct SmallParams {
   MultiCall c;
   int has_w;
+  int whole;                   // H~ is formed here, too
   int tile;                    // rows of X per tile (128, or 64 where shared memory holds no more)
   int t16;                     // MMA width: rows of a tile rounded up to 16
   int splits, kb_per, k_blocks;
@@ -189,6 +192,94 @@ struct SmallParams {
   uint32_t tmem_cols;
 };
 
+// The adapters' term of all of a few rows from this CTA's part of K, [c.T][128] in delta: h (the rows' rank
+// values over k0 .. k1, fp32) and then h B^T.  By 256 threads (tid), four rank rows a warp at a time.  The
+// parts' terms are added with their products of W, so H~ is never whole and is not rounded.
+__device__ __forceinline__ void whole_term(const MultiCall& c, float* delta, int n0, int k0, int k1, int tid) {
+  const int lane = tid & 31, w8 = tid >> 5;
+  const int ga = n0 / c.og, gb = min(n0 + 127, c.N - 1) / c.og;
+  const int nj = (gb - ga + 1) * c.R, rows = c.G * c.R;
+  float* h = delta + c.T * 128;                      // [c.T][nj]
+  auto slot_of = [&](int t, float& s) {
+    int a = c.slot[t];
+    s = 0.f;
+    if (a < 0 || a >= c.S) return -1;
+    s = c.scale[a];
+    if (c.row_scale) s = __fmul_rn(s, c.row_scale[t]);
+    s = __fmul_rn(s, c.request_scale);
+    return s != 0.f ? a : -1;
+  };
+  const int n = n0 + (tid & 127);
+  float s;
+  for (int t = tid >> 7; t < c.T && n < c.N; t += 2) {
+    const int a = slot_of(t, s);
+    if (a >= 0) prefetch_l2(c.B + (static_cast<long long>(a) * c.N + n) * c.R);
+  }
+  const int quads = nj / 4;
+  for (int t = 0; t < c.T; ++t) {
+    const int a = slot_of(t, s);
+    if (a < 0) continue;
+    const uint16_t* x = c.X + t * c.ldx;
+    for (int q = w8; q < quads; q += 8) {
+      const uint16_t* A = c.A + (static_cast<long long>(a) * rows + ga * c.R + q * 4) * c.K;
+      F2 sum[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = f2(0.f, 0.f);
+      for (int k = k0 + lane * 8; k < k1; k += 256) {
+        const uint4 xv = ldg16(x + k);
+        uint4 av[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) av[i] = ldg16(A + static_cast<long long>(i) * c.K + k);
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t aw[4] = {av[i].x, av[i].y, av[i].z, av[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sum[i] = f2_fma(f2(__uint_as_float(xw[e] << 16), __uint_as_float(xw[e] & 0xffff0000u)),
+                            f2(__uint_as_float(aw[e] << 16), __uint_as_float(aw[e] & 0xffff0000u)), sum[i]);
+        }
+      }
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a0, a1;
+        f2_get(sum[i], a0, a1);
+        v[i] = a0 + a1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      }
+      if (lane == 0) *reinterpret_cast<float4*>(h + t * nj + q * 4) = make_float4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
+    }
+  }
+  named_bar_sync(1, 256);
+  for (int t = tid >> 7; t < c.T; t += 2) {
+    const int a = slot_of(t, s);
+    float v = 0.f;
+    if (a >= 0 && n < c.N) {
+      const uint16_t* b = c.B + (static_cast<long long>(a) * c.N + n) * c.R;
+      const float* hg = h + t * nj + (n / c.og - ga) * c.R;
+#pragma unroll 4
+      for (int r = 0; r < c.R; r += 8) {
+        const uint4 bv = ldg16(b + r);
+        const float4 h0 = *reinterpret_cast<const float4*>(hg + r), h1 = *reinterpret_cast<const float4*>(hg + r + 4);
+        v = fmaf(h0.x, __uint_as_float(bv.x << 16), v);
+        v = fmaf(h0.y, __uint_as_float(bv.x & 0xffff0000u), v);
+        v = fmaf(h0.z, __uint_as_float(bv.y << 16), v);
+        v = fmaf(h0.w, __uint_as_float(bv.y & 0xffff0000u), v);
+        v = fmaf(h1.x, __uint_as_float(bv.z << 16), v);
+        v = fmaf(h1.y, __uint_as_float(bv.z & 0xffff0000u), v);
+        v = fmaf(h1.z, __uint_as_float(bv.w << 16), v);
+        v = fmaf(h1.w, __uint_as_float(bv.w & 0xffff0000u), v);
+      }
+    }
+    delta[t * 128 + (tid & 127)] = v;
+  }
+  named_bar_sync(1, 256);
+}
+
+// kWhole: H~ is formed here, too.
+template <bool kWhole>
 __global__ void __launch_bounds__(kSmallThreads, 2)
     multi_small_kernel(const __grid_constant__ SmallMaps maps, const __grid_constant__ SmallParams p) {
   const MultiCall& c = p.c;
@@ -289,7 +380,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     const int row = (warp & 3) * 32 + lane;           // output column n0 + row = TMEM lane
     const int w8 = warp - 2;                          // 0..7
     const int half = w8 >> 2;
-    adapters_term(c, term, delta, t0 + r0, cnt, n0, threadIdx.x - 64);
+    if (kWhole) whole_term(c, delta, n0, kb0 * kBK, min(c.K, kb1 * kBK), threadIdx.x - 64);
+    else adapters_term(c, term, delta, t0 + r0, cnt, n0, threadIdx.x - 64);
+    // (whole: the few rows' terms join their products of W here)
+    auto own = [&](int t) { return kWhole && t < c.T ? delta[t * 128 + row] : 0.f; };
     // ------------------------------------------------ the accumulator into shared memory
     if (p.has_w) {
       const bool ok = mbar_wait(&acc_full, 0, abort_flag, tmo, status);
@@ -300,12 +394,14 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
           uint32_t r8[8];
           tmem_ld8(tmem + lane_base + col, r8);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) part[(col + i) * 128 + row] = __uint_as_float(r8[i]);
+          for (int i = 0; i < 8; ++i) part[(col + i) * 128 + row] = __uint_as_float(r8[i]) + own(col + i);
         }
         tc_fence_before();
       } else {
-        for (int col = half; col < p.t16; col += 2) part[col * 128 + row] = 0.f;
+        for (int col = half; col < p.t16; col += 2) part[col * 128 + row] = own(col);
       }
+    } else if (kWhole) {
+      for (int t = half; t < c.T; t += 2) part[t * 128 + row] = own(t);
     }
   }
   __syncthreads();
@@ -321,7 +417,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     }
     for (int i = warp - 2; i < cnt; i += 8) {
       float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (p.has_w) {
+      if (p.has_w || kWhole) {
         const uint32_t at = smem_u32(part + (r0 + i) * 128 + lane * 4);
         if (p.splits > 1) {
           float4 q[8];
@@ -342,7 +438,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
           v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
         }
       }
-      const float4 d = *reinterpret_cast<const float4*>(delta + i * 128 + lane * 4);
+      const float4 d = kWhole ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(delta + i * 128 + lane * 4);
       v[0] = (v[0] + bias[0]) + d.x;
       v[1] = (v[1] + bias[1]) + d.y;
       v[2] = (v[2] + bias[2]) + d.z;
@@ -373,6 +469,17 @@ int fail(cudaError_t e) {
 
 }  // namespace
 
+// Rank rows of the column groups that a tile of 128 columns can meet
+static int ranks_of_tile(const MultiCall& c) {
+  return c.og % 128 == 0 ? c.R : c.R * std::min(c.G, 127 / c.og + 2);
+}
+
+// One or two rows of few ranks: every tile's CTAs read the rows' A again (from L2) and save the first
+// kernel.  One row took 7.1 us so and 7.9 with both kernels (1536 -> 3 x 1536, rank 32), 9.7 and 11.2
+// (4096 -> 4096, rank 16), 13.5 and 14.3 (5120 -> 5120, rank 64), besides a launch's time on the host; two rows
+// of rank 32 8.0 and 8.6, but two of rank 64 11.8 and 10.8 (1536 -> 8960), three of rank 16 14.8 and 13.4.
+bool multi_whole(const MultiCall& c) { return c.T <= 2 && c.T * ranks_of_tile(c) <= 64; }
+
 int launch_multi_shrink_small(const MultiCall& c, cudaStream_t stream) {
   // a sweep of a CTA's warps covers 1024 of K; up to four CTAs share a longer K while the grid stays
   // within eight CTAs per SM (most of a grid leaves at once where rows share slots)
@@ -400,13 +507,16 @@ int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStr
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail(e);
   if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1u)) {
-    e = cudaFuncSetAttribute(multi_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+    e = cudaFuncSetAttribute(multi_small_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(multi_small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
     if (e != cudaSuccess) return fail(e);
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   SmallParams p{};
   p.c = c;
   p.has_w = W ? 1 : 0;
+  p.whole = multi_whole(c) ? 1 : 0;
   p.k_blocks = (c.K + kBK - 1) / kBK;
   const int n_tiles = (c.N + 127) / 128;
   int t_tiles = 0;
@@ -434,7 +544,7 @@ int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStr
     p.kb_per = (p.k_blocks + p.splits - 1) / p.splits;
     p.share = (tile + p.splits - 1) / p.splits;
     p.stage_bytes = kATileBytes + p.t16 * 128;
-    const int delta_bytes = p.share * 128 * 4;
+    const int delta_bytes = p.whole ? c.T * (512 + ranks_of_tile(c) * 4) : p.share * 128 * 4;
     p.stages = (kSmallSmem - 1024 - delta_bytes) / p.stage_bytes;
     if (p.stages > kSmallMaxStages) p.stages = kSmallMaxStages;
     if (p.stages > p.kb_per) p.stages = p.kb_per;
@@ -459,9 +569,11 @@ int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStr
   attr[1].val.clusterDim.x = p.splits;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, multi_small_kernel, maps, p);
+  // alone, the kernel starts after what came before it in the stream
+  cfg.attrs = p.whole ? attr + 1 : attr;
+  cfg.numAttrs = p.whole ? 1 : 2;
+  e = p.whole ? cudaLaunchKernelEx(&cfg, multi_small_kernel<true>, maps, p)
+              : cudaLaunchKernelEx(&cfg, multi_small_kernel<false>, maps, p);
   return e == cudaSuccess ? WP_OK : fail(e);
 }
 
