@@ -18,15 +18,15 @@
 // atomics, the same bits each time.
 //
 // Measured (device time; bytes read and written once over it; a copy reaches 6.8 TB/s):
-//   32760 x 1536 bf16   forward 34 us, 5.9 TB/s; backward 65 us, 4.7 TB/s (of it 9 us until the first
-//                       rows are there and 5 us for the second kernel; between them 5.9 TB/s)
-//   8000 x 5120 fp32    forward 56 us, 5.9 TB/s; backward 83 us, 5.9 TB/s
+//   32760 x 1536 bf16   forward 34 us, 5.9 TB/s; backward 57 us, 5.3 TB/s, the first rows' arrival and the
+//                       second kernel included
+//   16000 x 5120 fp32   forward 114 us, 5.8 TB/s; backward 153 us, 6.4 TB/s
 //   16 x 5120 bf16      forward 3.5 us, of which a launch is most
 //   20000 x 2187 bf16   forward 70 us, 2.5 TB/s; backward 116 us, 2.3 TB/s: the shifts, twice the
 //                       arithmetic of an aligned row, are what bounds these
 //   8000 x 4099 fp32    forward 93 us, 2.8 TB/s; backward 124 us, 3.2 TB/s
 // Shifted rows were read and written element by element first: 96 and 278 us, 102 and 161 us.  Their
-// backward takes half the rows a turn of an aligned one's: with as many, the registers spill (221 us).
+// backward takes half the rows a turn of an aligned one's: with as many, the registers spill.
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -978,34 +978,38 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_long_kernel(const NormPa
   }
 }
 
-// dw, db [C] from the CTAs' partial rows: 32 columns a block, 16 warps take every sixteenth partial
-// row, joined in warp order.  Launched beside the backward (its blocks wait for it to finish).
+// dw, db [C] from the CTAs' partial rows: 8 columns a block (one sector of a row), a thread every 64th row
+// of a column, eight loads at a time, joined in order.  Launched beside the backward (its blocks wait
+// for it to finish).
+constexpr int kFinishCols = 8;
 __global__ void __launch_bounds__(512) norm_finish_kernel(const float* part, int n, int C, float* dw, float* db) {
-  __shared__ float sh[16][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  constexpr int kRows = 512 / kFinishCols;
+  __shared__ float sh[kRows][kFinishCols + 1];
+  const int col = threadIdx.x % kFinishCols, sub = threadIdx.x / kFinishCols;
+  const int c = blockIdx.x * kFinishCols + col;
   float* out = blockIdx.y ? db : dw;
   grid_dependency_wait();
   if (!out) return;
   const float* q = part + static_cast<long long>(blockIdx.y) * C + c;
   float s = 0.f;
   if (c < C) {
-    for (int i0 = warp; i0 < n; i0 += 16 * 8) {
+    for (int i0 = sub; i0 < n; i0 += kRows * 8) {
       float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = i0 + 16 * k < n ? q[static_cast<long long>(i0 + 16 * k) * 2 * C] : 0.f;
+      for (int k = 0; k < 8; ++k) v[k] = i0 + kRows * k < n ? q[static_cast<long long>(i0 + kRows * k) * 2 * C] : 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) s += v[k];
     }
   }
-  sh[warp][lane] = s;
+  sh[sub][col] = s;
   __syncthreads();
-  if (warp == 0 && c < C) {
-    float t = sh[0][lane];
+  if (threadIdx.x >= 4 * kFinishCols) return;          // four threads a column, then one
+  float t = 0.f;
 #pragma unroll
-    for (int i = 1; i < 16; ++i) t += sh[i][lane];
-    out[c] = t;
-  }
+  for (int i = 0; i < kRows / 4; ++i) t += sh[sub * (kRows / 4) + i][col];
+  t += __shfl_xor_sync(0xffffffffu, t, kFinishCols);
+  t += __shfl_xor_sync(0xffffffffu, t, 2 * kFinishCols);
+  if (sub == 0 && c < C) out[c] = t;
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1052,48 +1056,55 @@ bool ring_form(Form* f, long long C, bool f32, bool vec, int ops) {
   return f->stages >= 2;
 }
 
-// Forward: 16 or so elements a thread and four rows a turn, so that what a turn costs besides its
-// elements (waits, sums, barriers) is spread over 64; longer rows take more elements and fewer rows.
-Form fwd_form(long long C, bool f32, bool vec) {
+// A form that takes nv vectors a thread and up to `top` threads; worth: its rate beside the first one's
+// where both fill the schedulers (it has fewer rows a turn to spread the turn's waits over, or spills).
+struct Option {
+  int nv, rows, top, regs;
+  double worth;
+};
+
+// The form with the most of the schedulers' warps at work: lanes that have columns, times the warps that
+// the CTAs on an SM occupy of 16, times its worth; a CTA alone on its SM has nothing to run while its
+// rows' sums meet, and counts four fifths.  Backward, 32760 rows of bf16: 2560 columns took 124 us with
+// ten warps of 8 elements a thread and 90 with five of 16, 1280 columns 52 and 60, 4096 columns 155
+// and 138.
+template <int kOptions>
+Form pick_form(const Option (&options)[kOptions], long long C, bool f32, bool vec, int ops) {
   const long long n = (C + (f32 ? 3 : 7)) / (f32 ? 4 : 8);
-  Form f{0, 1, kMaxThreads, 64, 2, 0, 0};
-  if (C > (1 << 20)) return f;
-  struct { int nv, rows, top, regs; } const forms[] = {{1, 4, 64, 104}, {2, 4, 512, 128}, {4, 2, 512, 128}, {8, 1, 512, 128}};
-  for (const auto& q : forms) {
-    if (n <= static_cast<long long>(q.nv) * q.top) {
-      f.nv = q.nv;
-      f.rows = q.rows;
-      f.regs = q.regs;
-      f.threads = row_threads(n, q.nv);
-      break;
+  Form best{0, 1, kMaxThreads, 64, 2, 0, 0};
+  if (C > (1 << 20)) return best;
+  double most = 0;
+  for (const Option& q : options) {
+    if (n > static_cast<long long>(q.nv) * q.top) continue;
+    Form f{q.nv, q.rows, row_threads(n, q.nv), q.regs, 0, 0, 0};
+    if (!ring_form(&f, C, f32, vec, ops)) continue;
+    const double rate = static_cast<double>(n) / (q.nv * f.threads) * (f.per_sm * f.threads) / 512 * q.worth *
+                        (f.per_sm == 1 ? 0.8 : 1);
+    if (rate > most) {
+      most = rate;
+      best = f;
     }
   }
-  if (f.nv && !ring_form(&f, C, f32, vec, 1)) f = Form{0, 1, kMaxThreads, 64, 2, 0, 0};
-  return f;
+  return best;
+}
+
+// Forward: 8 elements a thread (short rows), 16 and four rows a turn, or more and fewer rows.  Aligned rows
+// wait for memory whatever the warps and take the first form that holds them (8192 columns of bf16 took
+// 159 us with 16 warps of 16 elements and 190 with 8 of 32); shifted ones are bound by instructions (4099
+// columns of bf16 260 us with nine warps of 16, 212 with five of 32).
+Form fwd_form(long long C, bool f32, bool vec) {
+  const Option first[] = {{1, 4, 64, 104, 1}, {2, 4, 512, 128, 0.1}, {4, 2, 512, 128, 0.01}, {8, 1, 512, 128, 0.001}},
+               shifted[] = {{1, 4, 64, 104, 1}, {2, 4, 512, 128, 1}, {4, 2, 512, 128, 0.75}, {8, 1, 512, 128, 0.3}};
+  return vec ? pick_form(first, C, f32, true, 1) : pick_form(shifted, C, f32, false, 1);
 }
 
 // Backward: 8 elements a thread and four rows a turn (its dw, db, weight, xh and h take registers
-// each), 16 and two, or 32 and one.  Shifted rows take half as many rows a turn, and 8 elements a thread
-// only up to 256 threads, so that two CTAs fit an SM: 2187 columns of bf16 took 161 us with 288 threads
-// of 8 elements and 116 with 160 of 16, 2801 columns 164 and 148 (20000 rows).
+// each), 16 and two, or 32 and one; shifted rows half as many rows a turn.
 Form bwd_form(long long C, bool f32, bool vec) {
-  const long long n = (C + (f32 ? 3 : 7)) / (f32 ? 4 : 8);
-  Form f{0, 1, kMaxThreads, 64, 2, 0, 0};
-  if (C > (1 << 20)) return f;
-  struct { int nv, rows, top, regs; } const v8[] = {{1, 4, 512, 128}, {2, 2, 512, 128}, {4, 1, 512, 128}, {4, 1, 512, 128}},
-                                            v4[] = {{2, 4, 512, 128}, {4, 2, 512, 128}, {8, 1, 512, 128}, {8, 1, 512, 128}};
-  for (int i = 0; i < 4; ++i) {
-    const auto& q = f32 ? v4[i] : v8[i];
-    if (n <= static_cast<long long>(q.nv) * (!vec && q.rows == 4 ? 256 : q.top)) {
-      f.nv = q.nv;
-      f.rows = vec ? q.rows : (q.rows + 1) / 2;
-      f.regs = q.regs;
-      f.threads = row_threads(n, q.nv);
-      break;
-    }
-  }
-  if (f.nv && !ring_form(&f, C, f32, vec, 2)) f = Form{0, 1, kMaxThreads, 64, 2, 0, 0};
-  return f;
+  const int h = vec ? 1 : 2;
+  const Option v8[] = {{1, 4 / h, 512, 128, 1}, {2, 2 / h, 512, 128, 0.9}, {4, 1, 512, 128, vec ? 0.45 : 0.6}},
+               v4[] = {{2, 4 / h, 512, 128, 1}, {4, 2 / h, 512, 128, 0.75}, {8, 1, 512, 128, 0.4}};
+  return f32 ? pick_form(v4, C, true, vec, 2) : pick_form(v8, C, false, vec, 2);
 }
 
 template <typename K>
@@ -1302,7 +1313,7 @@ int lora_norm_bwd(const wp_mat* dY, const wp_mat* X, const wp_mat* weight, const
                                      : dispatch_bwd<float>(p, vec, layer, &grid, st);
   if (rc != WP_OK || !sums) return rc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.C + 31) / 32, 2);
+  cfg.gridDim = dim3((p.C + kFinishCols - 1) / kFinishCols, 2);
   cfg.blockDim = dim3(512);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
