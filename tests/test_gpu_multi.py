@@ -213,3 +213,15 @@ def test_one_or_two_rows(K, N, G, R, base, T):
         y = lay.check(slot[:T], 0.6)
         assert torch.equal(lay.run(slot[:T], 0.6), y)
     lay.check([0, 2][:T], 1.0, row_scale=False, out_dtype=torch.float32)
+
+
+@pytest.mark.parametrize("T", [3, 4, 13, 16, 17, 31, 64, 90])
+@pytest.mark.parametrize("base", ["bf16", "nf4", None])
+@pytest.mark.parametrize("K,N,G,R", [(512, 1000, 1, 16), (1536, 120, 3, 8), (256, 48, 6, 16), (2048, 192, 8, 8)])
+def test_rows_with_a_slot_each(K, N, G, R, base, T):
+    lay = Layer(T, K, N, G, R, 100, base=base, bias="bf16", seed=N + T)
+    slot = [int(v) for v in np.random.default_rng(T).permutation(100)[:T]]
+    lay.check(slot, 0.9)
+    for i in range(0, T, 3):
+        slot[i] = -1
+    lay.check(slot, 0.9)

@@ -14,7 +14,7 @@
 // between a block's load and its sums; two spans of 256 k are on their way while one is worked on.
 // K is cut into parts, whose fp32 sums meet in the second kernel with the bias and the adapters' term.
 //
-// Measured, 28672 x 4096 and 16 slots of rank 16: 16 rows 39 us (this kernel 28, permutes alone 34; the
+// Measured, 28672 x 4096 and 16 slots of rank 16: 16 rows 37 us (this kernel 28, permutes alone 34; the
 // codes take 9 from HBM), 1 row 28, 64 rows 79.  With the decoding in warps of its own and
 // tcgen05.mma on tiles in shared memory the 16 rows took 54 us, the 64 rows 73; five other layers 12-64 us
 // where this takes 9-55.

@@ -33,6 +33,67 @@ struct TermShared {
   __align__(8) uint8_t g_row[kTermRows][8];
 };
 
+// Up to 16 rows, most with a slot of their own, of rank 8 or 16: an mma.sync would use one row of its eight,
+// and its chain H~, products, next groups is what the rest of the kernel waits for.  A thread takes a
+// column and every other row; all of its B is on its way to registers before H~ is waited for, and H~
+// comes to shared memory (in delta's place) at once.  64 rows of 64 slots of rank 16 beside 5120 -> 5120:
+// 21.4 us by groups, 19.7 so; 16 rows of 16 beside the 4-bit 4096 -> 28672 39.7 and 36.9.  At
+// larger ranks a column's B no longer comes in one piece: 16 rows of rank 64 25 and 34.5.
+constexpr int kTermSingles = 8;                      // rows a thread
+__device__ __forceinline__ void singles_term(const MultiCall& c, const TermShared& sh, float* delta, int first, int cnt,
+                                             int n0, int c0, int wide, int tid) {
+  const int col = tid & 127, n = min(n0 + col, c.N - 1);
+  auto load = [&](int r, uint4 (&v)[kTermSingles]) {
+#pragma unroll
+    for (int k = 0; k < kTermSingles; ++k) {
+      const int i = (tid >> 7) + 2 * k, a = i < cnt && r < c.R ? sh.act[i] : -1;
+      v[k] = a >= 0 ? ldg16(c.B + (static_cast<long long>(a) * c.N + n) * c.R + r) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint4 b0[kTermSingles], b1[kTermSingles];
+  load(0, b0);
+  load(8, b1);
+  grid_dependency_wait();
+  uint16_t* h = reinterpret_cast<uint16_t*>(delta);  // [cnt][wide]
+  const int pieces = wide / 8;
+  for (int p = tid; p < cnt * pieces; p += 256) {
+    const int i = p / pieces, o = (p - i * pieces) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (sh.act[i] >= 0)
+      v = *reinterpret_cast<const uint4*>(c.H + (static_cast<long long>(first + i) * c.G + c0) * c.R16 + o);
+    *reinterpret_cast<uint4*>(h + i * wide + o) = v;
+  }
+  named_bar_sync(1, 256);
+  F2 sum[kTermSingles];
+#pragma unroll
+  for (int k = 0; k < kTermSingles; ++k) sum[k] = f2(0.f, 0.f);
+  const uint16_t* hg = h + (n / c.og - c0) * c.R16;
+  auto add = [&](int r, const uint4 (&v)[kTermSingles]) {
+    if (r >= c.R) return;
+#pragma unroll
+    for (int k = 0; k < kTermSingles; ++k) {
+      const int i = (tid >> 7) + 2 * k;
+      if (i >= cnt) continue;
+      const uint4 q = *reinterpret_cast<const uint4*>(hg + i * wide + r);
+      const uint32_t hw[4] = {q.x, q.y, q.z, q.w}, bw[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sum[k] = f2_fma(f2(__uint_as_float(hw[e] << 16), __uint_as_float(hw[e] & 0xffff0000u)),
+                        f2(__uint_as_float(bw[e] << 16), __uint_as_float(bw[e] & 0xffff0000u)), sum[k]);
+    }
+  };
+  add(0, b0);
+  add(8, b1);
+  named_bar_sync(1, 256);                            // H~ has been read
+#pragma unroll
+  for (int k = 0; k < kTermSingles; ++k) {
+    float x, y;
+    f2_get(sum[k], x, y);
+    const int i = (tid >> 7) + 2 * k;
+    if (i < cnt) delta[i * 128 + col] = x + y;
+  }
+}
+
 // delta[i][128 columns from n0] of the cnt (<= kTermRows) rows from `first` on, by 256 threads (tid; named
 // barrier 1), 16 columns a warp.  The slots and scales are inputs, so only H~ waits for the kernel before
 // (whose end every thread has waited for on return).  The caller passes a barrier before it
@@ -72,6 +133,11 @@ __device__ __forceinline__ void adapters_term(const MultiCall& c, TermShared& sh
   for (int w = 0; w < 4; ++w) {
     if (w < w8) gid += sh.g_count[w];
     ng += sh.g_count[w];
+  }
+  const int c0 = n0 / c.og, wide = (min(n0 + 127, c.N - 1) / c.og - c0 + 1) * c.R16;
+  if (c.R <= 16 && cnt <= 2 * kTermSingles && cnt <= 2 * ng && wide <= 256) {
+    singles_term(c, sh, delta, first, cnt, n0, c0, wide, tid);
+    return;
   }
   if (leads) {
     sh.g_slot[gid] = a;
