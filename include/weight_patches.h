@@ -409,7 +409,8 @@ typedef struct wp_bank {
  * A row's result depends on that row and its adapter alone: a row without an adapter, or whose
  * s_t is exactly 0, equals the row of the plain projection, and values that are not finite in
  * one slot or row do not reach rows of other slots.  As in lora_linear_fwd, s X A^T is rounded
- * once to bf16, sums are fp32 and the output is rounded once.
+ * once to bf16 (one or two rows of few ranks keep it in fp32), sums are fp32 and the output is
+ * rounded once.
  *   workspace: lora_multi_workspace_size(X, W, bank) bytes, 16-byte aligned.
  * Alignment: as lora_linear_fwd's tensor-core path (16-byte bases and pitches, in % 8 == 0,
  * out_g % 8 == 0); n_groups <= 8.  Errors as lora_linear_fwd; WP_ERR_DTYPE for a bank that is
