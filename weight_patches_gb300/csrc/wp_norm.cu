@@ -1065,9 +1065,10 @@ struct Option {
 
 // The form with the most of the schedulers' warps at work: lanes that have columns, times the warps that
 // the CTAs on an SM occupy of 16, times its worth; a CTA alone on its SM has nothing to run while its
-// rows' sums meet, and counts four fifths.  Backward, 32760 rows of bf16: 2560 columns took 124 us with
-// ten warps of 8 elements a thread and 90 with five of 16, 1280 columns 52 and 60, 4096 columns 155
-// and 138.
+// rows' sums meet, and counts four fifths; one warp needs no CTA barrier, which is a gain where rows are
+// shifted (60000 x 509 bf16 backward 78 us with two warps, 70 with one).  Backward, 32760 rows of bf16:
+// 2560 columns took 124 us with ten warps of 8 elements a thread and 90 with five of 16, 1280 columns 52
+// and 60, 4096 columns 155 and 138.
 template <int kOptions>
 Form pick_form(const Option (&options)[kOptions], long long C, bool f32, bool vec, int ops) {
   const long long n = (C + (f32 ? 3 : 7)) / (f32 ? 4 : 8);
@@ -1079,7 +1080,7 @@ Form pick_form(const Option (&options)[kOptions], long long C, bool f32, bool ve
     Form f{q.nv, q.rows, row_threads(n, q.nv), q.regs, 0, 0, 0};
     if (!ring_form(&f, C, f32, vec, ops)) continue;
     const double rate = static_cast<double>(n) / (q.nv * f.threads) * (f.per_sm * f.threads) / 512 * q.worth *
-                        (f.per_sm == 1 ? 0.8 : 1);
+                        (f.per_sm == 1 ? 0.8 : f.threads == 32 && !vec ? 1.3 : 1);
     if (rate > most) {
       most = rate;
       best = f;
@@ -1088,13 +1089,14 @@ Form pick_form(const Option (&options)[kOptions], long long C, bool f32, bool ve
   return best;
 }
 
-// Forward: 8 elements a thread (short rows), 16 and four rows a turn, or more and fewer rows.  Aligned rows
+// Forward: 8 elements a thread (rows of up to 32 vectors, one warp; two warps of it took 27 us for 60000 x
+// 512 bf16 where one of 16 elements takes 21), 16 and four rows a turn, or more and fewer rows.  Aligned rows
 // wait for memory whatever the warps and take the first form that holds them (8192 columns of bf16 took
 // 159 us with 16 warps of 16 elements and 190 with 8 of 32); shifted ones are bound by instructions (4099
 // columns of bf16 260 us with nine warps of 16, 212 with five of 32).
 Form fwd_form(long long C, bool f32, bool vec) {
-  const Option first[] = {{1, 4, 64, 104, 1}, {2, 4, 512, 128, 0.1}, {4, 2, 512, 128, 0.01}, {8, 1, 512, 128, 0.001}},
-               shifted[] = {{1, 4, 64, 104, 1}, {2, 4, 512, 128, 1}, {4, 2, 512, 128, 0.75}, {8, 1, 512, 128, 0.3}};
+  const Option first[] = {{1, 4, 32, 104, 1}, {2, 4, 512, 128, 0.1}, {4, 2, 512, 128, 0.01}, {8, 1, 512, 128, 0.001}},
+               shifted[] = {{1, 4, 32, 104, 1}, {2, 4, 512, 128, 1}, {4, 2, 512, 128, 0.75}, {8, 1, 512, 128, 0.3}};
   return vec ? pick_form(first, C, f32, true, 1) : pick_form(shifted, C, f32, false, 1);
 }
 
