@@ -225,3 +225,12 @@ def test_rows_with_a_slot_each(K, N, G, R, base, T):
     for i in range(0, T, 3):
         slot[i] = -1
     lay.check(slot, 0.9)
+
+
+@pytest.mark.parametrize("base", ["bf16", "nf4"])
+def test_a_workspace_for_more_rows_serves_fewer(base):
+    big = Layer(700, 512, 5136, 1, 16, 5, base=base, seed=1)
+    size = wpg.lora_multi_workspace_size(big.X, big.W, big.bank)
+    for T in (1, 64, 120, 300):
+        lay = Layer(T, 512, 5136, 1, 16, 5, base=base, seed=T)
+        lay.check(_slots(T, 5, "any", T), workspace=torch.empty(size, dtype=torch.uint8, device=gu.DEV))

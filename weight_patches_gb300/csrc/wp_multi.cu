@@ -119,7 +119,12 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
   if (!al16(X->data) || X->ld % 8 || !al16(bank->A) || !al16(bank->B)) return WP_ERR_ALIGN;
   if (W && (!al16(W->data) || W->ld % 8)) return WP_ERR_ALIGN;
   if (!al16(Y->data) || Y->ld % (Y->dtype == WP_BF16 ? 8 : 4)) return WP_ERR_ALIGN;
-  const Layout L = layout(X, W, bank);
+  Layout L = layout(X, W, bank);
+  // a workspace sized for more rows may lack the partial sums of a few: those then go the way of many
+  if (L.parts && workspace_bytes < L.total) {
+    L.parts = 0;
+    L.total = L.part;
+  }
   if (!workspace || workspace_bytes < L.total) return WP_ERR_WORKSPACE;
   if (!al16(workspace)) return WP_ERR_ALIGN;
 
