@@ -523,7 +523,6 @@ struct MultiCall {
   const float* row_scale;
   float request_scale;
   uint16_t* H;                           // [T, G R16] bf16: s X A^T
-  int* act;                              // [T]: the row's slot, or -1 when it uses no adapter
   float* srow;                           // [T]: s_t (many rows)
   MultiEntry* ent;                       // [blocks of 256 rows][ent_ld] (many rows)
   int* ent_n;

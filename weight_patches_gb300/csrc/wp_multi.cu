@@ -60,10 +60,10 @@ bool nf4_few(long long T, const wp_mat* W) {
 }
 bool small_rows(int T, const wp_mat* W) { return T <= kSmallRows && (!W || W->dtype == WP_BF16); }
 
-// H~ [T, G R16] | act [T] (few rows), or s [T] | entries | their counts | rows with an adapter
+// H~ [T, G R16] | s [T] (many rows) | entries | their counts | rows with an adapter
 // the K splits' partial sums (a 4-bit weight, few rows) come last
 struct Layout {
-  size_t act = 0, ent = 0, ent_n = 0, ent_rows = 0, part = 0, total = 0;
+  size_t srow = 0, ent = 0, ent_n = 0, ent_rows = 0, part = 0, total = 0;
   int ent_ld = 0;
   int parts = 0;                          // of K, few rows over a 4-bit weight
 };
@@ -72,8 +72,8 @@ Layout layout(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
   Layout L;
   const size_t T = static_cast<size_t>(X->rows), blocks = (T + 255) / 256;
   const size_t r16 = (bank->rank + 15) / 16 * 16;
-  L.act = r256(T * bank->n_groups * r16 * 2);
-  L.total = L.ent = L.act + r256(T * 4);
+  L.srow = r256(T * bank->n_groups * r16 * 2);
+  L.total = L.ent = L.srow + r256(T * 4);
   if (!small_rows(static_cast<int>(T < (1u << 30) ? T : (1u << 30)), W)) {
     L.ent_ld = bank->n_slots < 256 ? bank->n_slots : 256;
     L.ent_n = L.ent + r256(blocks * L.ent_ld * sizeof(MultiEntry));
@@ -137,7 +137,6 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
   c.A = static_cast<const uint16_t*>(bank->A); c.B = static_cast<const uint16_t*>(bank->B);
   c.scale = bank->scale; c.slot = slot; c.row_scale = row_scale; c.request_scale = rs;
   c.H = reinterpret_cast<uint16_t*>(ws);
-  c.act = reinterpret_cast<int*>(ws + L.act);
   if (bias) {
     c.bias = bias->data;
     c.bias_f32 = bias->dtype == WP_FP32;
@@ -160,7 +159,7 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
     if (rc != WP_OK) return rc;
     return launch_multi_nf4(c, W->data, W->absmax, reinterpret_cast<float*>(ws + L.part), L.parts, st);
   }
-  c.srow = reinterpret_cast<float*>(ws + L.act);
+  c.srow = reinterpret_cast<float*>(ws + L.srow);
   c.ent = reinterpret_cast<MultiEntry*>(ws + L.ent);
   c.ent_n = reinterpret_cast<int*>(ws + L.ent_n);
   c.ent_rows = reinterpret_cast<uint32_t*>(ws + L.ent_rows);

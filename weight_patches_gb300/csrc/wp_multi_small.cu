@@ -98,10 +98,7 @@ __global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_launch_dependents();
   const int a = c.slot[t];
-  if (a < 0 || a >= c.S) {
-    if (chunk == 0 && part == 0 && tid == 0) c.act[t] = -1;
-    return;
-  }
+  if (a < 0 || a >= c.S) return;                     // the same in every CTA of the cluster
   // the rows of this slot in order, 32 to a pass; the first of each pass stands for it
   int before = 0, n = 0;
   for (int base = 0; base < c.T; base += kShrinkThreads) {
@@ -163,7 +160,6 @@ __global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(cons
         asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(hb) : "f"(h * s));
         *out = hb;
         if (c.R != c.R16 && rr >= c.R - 8) out[8] = 0;   // the group's padding columns
-        if (j == 0) c.act[tt] = s != 0.f ? a : -1;
       }
     }
   }
