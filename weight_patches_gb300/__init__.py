@@ -245,6 +245,25 @@ def _pout(t: torch.Tensor) -> bytes:
     return _pmat(t)[:40]                          # wp_out: wp_mat without its last pointer
 
 
+def _one_device(call: str, first: torch.Tensor, *others) -> int:
+    """The index of the CUDA device that all of a call's tensors lie on (None: an argument not given).
+    A kernel would read a host pointer as its own memory."""
+    index = first.get_device()
+    for t in others:
+        if t is None:
+            continue
+        if isinstance(t, NF4Weight):
+            if t.absmax.get_device() != index:
+                break
+            t = t.packed
+        if t.get_device() != index:
+            break
+    else:
+        if index >= 0:
+            return index
+    raise ValueError(f"{call}: its tensors must be on one CUDA device")
+
+
 def _check(status: int, where: str):
     if status != 0:
         raise WeightPatchesError(status, where)
@@ -492,6 +511,7 @@ def lora_linear_fwd_multi(X: torch.Tensor, W, bias: Optional[torch.Tensor], bank
     if row_scale is not None and (row_scale.dtype is not torch.float32 or row_scale.numel() != T
                                   or not row_scale.is_contiguous()):
         raise ValueError("row_scale must be a contiguous float32 tensor with one entry per row of X")
+    device = _one_device("lora_linear_fwd_multi", X, W, bias, bank.A, slot, row_scale, out, workspace)
     if out is None:
         out = torch.empty(T, bank.out_features, dtype=out_dtype, device=X.device)
     lib = _load()
@@ -500,7 +520,7 @@ def lora_linear_fwd_multi(X: torch.Tensor, W, bias: Optional[torch.Tensor], bank
     st = lib.lora_linear_fwd_multi(_pmat(X), _pmat(W), _pmat(bias), bank._packed, slot.data_ptr(),
                                    None if row_scale is None else row_scale.data_ptr(), request_scale, _pout(out),
                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                   _raw_stream(X.get_device()))
+                                   _raw_stream(device))
     if st:
         _check(st, "lora_linear_fwd_multi")
     return out
@@ -512,6 +532,7 @@ def lora_norm_fwd(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
                   stats: Optional[torch.Tensor] = None):
     """y = (x - mu) r w + b over the rows of X [T, C] (kind ``WP_NORM_RMS``: mu = 0).  Returns
     (y, stats), stats [2, T] fp32 holding mu and r for ``lora_norm_bwd``."""
+    device = _one_device("lora_norm_fwd", X, weight, bias, out, stats)
     if out is None:
         out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
     if stats is None:
@@ -519,7 +540,7 @@ def lora_norm_fwd(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
     else:
         _check_stats(stats, X.shape[0])
     st = _load().lora_norm_fwd(_pmat(X), _pvec(weight), _pvec(bias), kind, eps, _pout(out), stats.data_ptr(),
-                               _raw_stream(X.get_device()))
+                               _raw_stream(device))
     if st:
         _check(st, "lora_norm_fwd")
     return out, stats
@@ -535,6 +556,7 @@ def lora_norm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: Optional[torch.Tens
     """(dX, dW, dB) of ``lora_norm_fwd`` from its stats; dW and dB fp32 [C], None where not asked for."""
     T, C = X.shape
     _check_stats(stats, T)
+    device = _one_device("lora_norm_bwd", X, dY, weight, stats, workspace)
     dev = X.device
     dx = torch.empty(T, C, dtype=X.dtype, device=dev) if need_dx else None
     dw = torch.empty(C, dtype=torch.float32, device=dev) if need_dw else None
@@ -545,7 +567,7 @@ def lora_norm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: Optional[torch.Tens
                                None if dx is None else _pout(dx), None if dw is None else _pout(dw),
                                None if db is None else _pout(db), None if workspace is None else workspace.data_ptr(),
                                0 if workspace is None else workspace.numel() * workspace.element_size(),
-                               _raw_stream(X.get_device()))
+                               _raw_stream(device))
     if st:
         _check(st, "lora_norm_bwd")
     return dx, dw, db
@@ -616,6 +638,7 @@ def lora_adamw_plan(params: Sequence[torch.Tensor], m: Sequence, v: Sequence,
         arr[i] = WpAdamWTensor(p.data_ptr(), None if ma is None else ma.data_ptr(), parts[0][0].data_ptr(),
                                parts[1][0].data_ptr(), parts[2][0].data_ptr() if eight else None,
                                parts[3][0].data_ptr() if eight else None, numel, _DT[p.dtype], 8 if eight else 32)
+    _one_device("lora_adamw_plan", params[0])
     lib = _load()
     table = torch.empty(max(1, lib.lora_adamw_plan_size(arr, n)), dtype=torch.uint8, device=device)
     c = WpAdamWPlan()
@@ -644,10 +667,11 @@ def lora_adamw_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor]], lr
         raise ValueError("lora_adamw_step: a gradient has another dtype, size or layout than its tensor's")
     if grad_scale_tensor is not None and (grad_scale_tensor.dtype != torch.float32 or grad_scale_tensor.numel() != 1):
         raise ValueError("grad_scale_tensor must be one float32 value")
+    device = _one_device("lora_adamw_step", plan._table, grad_scale_tensor, *given)
     ptrs = plan._pack_ptrs(*[0 if g is None else g.data_ptr() for g in grads])
     args = _pack_adamw(lr, beta1, beta2, eps, weight_decay, grad_scale, step,
                        0 if grad_scale_tensor is None else grad_scale_tensor.data_ptr())
-    st = _load().lora_adamw_step(plan._packed, ptrs, _DT[dtype], args, _raw_stream(plan._table.get_device()))
+    st = _load().lora_adamw_step(plan._packed, ptrs, _DT[dtype], args, _raw_stream(device))
     if st:
         _check(st, "lora_adamw_step")
 
@@ -657,12 +681,13 @@ def lora_block8_decode(codes: torch.Tensor, absmax: torch.Tensor, out: Optional[
     if codes.dtype not in (torch.int8, torch.uint8) or not codes.is_contiguous() or not absmax.is_contiguous() \
             or absmax.dtype != torch.float32 or absmax.numel() != (codes.numel() + 255) // 256:
         raise ValueError("lora_block8_decode: contiguous int8 or uint8 codes and one fp32 scale per 256 of them")
+    device = _one_device("lora_block8_decode", codes, absmax, out)
     if out is None:
         out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
     elif out.dtype != torch.float32 or out.numel() != codes.numel() or not out.is_contiguous():
         raise ValueError("lora_block8_decode: out must be contiguous fp32 of the codes' size")
     _check(_load().lora_block8_decode(codes.data_ptr(), codes.dtype == torch.int8, absmax.data_ptr(), codes.numel(),
-                                      out.data_ptr(), _raw_stream(codes.get_device())), "lora_block8_decode")
+                                      out.data_ptr(), _raw_stream(device)), "lora_block8_decode")
     return out
 
 
