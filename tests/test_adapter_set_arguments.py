@@ -63,3 +63,49 @@ def test_one_tensor_on_the_host_is_refused(name):
             call(**{**tensors, k: tensors[k].cpu()})
     torch.cuda.synchronize()
     assert wpg.lora_device_status() == 0
+
+
+# ------------------------------------------------------------------------------ handles keep their memory
+def test_a_banks_tensors_cannot_be_exchanged():
+    A, B, scale = torch.zeros(2, 16, 64).bfloat16(), torch.zeros(2, 32, 16).bfloat16(), torch.ones(2)
+    bank = wpg.AdapterBank(A, B, scale)
+    for name, value in (("A", A.clone()), ("B", B.clone()), ("scale", scale.clone()), ("n_groups", 2), ("out_features", 8)):
+        with pytest.raises(AttributeError):
+            setattr(bank, name, value)
+    assert (bank.A is A and bank.B is B and bank.scale is scale) and (bank.n_groups, bank.out_features) == (1, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_plan_keeps_the_memory_it_updates(bits):
+    n = 1 << 20
+    p, g = torch.ones(n, device=DEV), torch.ones(n, device=DEV)
+    if bits == 8:
+        m, v = wpg.Block8.zeros(n, True, DEV), wpg.Block8.zeros(n, False, DEV)
+    else:
+        m, v = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    plan = wpg.lora_adamw_plan([p], [m], [v])
+    old = p.data_ptr()
+    p.data = torch.full((n,), 5.0, device=DEV)
+    if bits == 8:
+        m.codes, v.codes = m.codes.clone(), v.codes.clone()
+    else:
+        m.data, v.data = m.clone(), v.clone()
+    fresh = [torch.full((n,), 7.0, device=DEV) for _ in range(4)]
+    small = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    assert all(t.data_ptr() != old for t in fresh)
+    wpg.lora_adamw_step(plan, [g], 1e-3)
+    torch.cuda.synchronize()
+    assert bool((p == 5.0).all()) and all(bool((t == 7).all()) for t in fresh + small)
+
+
+@pytest.mark.gpu
+def test_a_bank_keeps_the_memory_it_reads():
+    A, B = torch.randn(2, 16, 64, device=DEV).bfloat16(), torch.randn(2, 32, 16, device=DEV).bfloat16()
+    scale, X = torch.ones(2, device=DEV), torch.randn(5, 64, device=DEV).bfloat16()
+    slot = torch.tensor([0, 1, 0, -1, 1], dtype=torch.int32, device=DEV)
+    bank = wpg.AdapterBank(A, B, scale)
+    want = wpg.lora_linear_fwd_multi(X, None, None, bank, slot)
+    scale.data, A.data, B.data = torch.zeros(2, device=DEV), torch.zeros_like(A), torch.zeros_like(B)
+    fresh = [torch.full_like(t, float("nan")) for t in (A, B, scale) for _ in range(3)]
+    assert torch.equal(wpg.lora_linear_fwd_multi(X, None, None, bank, slot), want) and len(fresh) == 9

@@ -474,7 +474,8 @@ class AdapterBank:
     """The adapters of one layer, one per slot, each padded with zeros to one rank:
     ``A`` [slots, n_groups * rank, in] and ``B`` [slots, out, rank] bf16, ``scale`` [slots] fp32
     (alpha / r * strength of each adapter), all contiguous on one device.  The tensors may be
-    rewritten in place (an adapter loaded into its slot) between calls."""
+    rewritten in place (an adapter loaded into its slot) between calls; they cannot be exchanged for
+    others: build another bank."""
 
     def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, n_groups: int = 1):
         if A.dim() != 3 or B.dim() != 3 or scale.dim() != 1:
@@ -487,11 +488,18 @@ class AdapterBank:
             raise ValueError("AdapterBank: the shapes of A, B and scale disagree")
         if not A.device == B.device == scale.device:
             raise ValueError("AdapterBank tensors must be on one device")
-        self.A, self.B, self.scale, self.n_groups = A, B, scale, n_groups
-        self.out_features = B.shape[1]
+        self._A, self._B, self._scale, self._n_groups = A, B, scale, n_groups
+        # aliases: the memory at the packed addresses lives as long as the bank does
+        self._kept = A.detach(), B.detach(), scale.detach()
         self._c = WpBank(A.data_ptr(), B.data_ptr(), scale.data_ptr(), _DT[A.dtype], A.shape[0], n_groups,
                          B.shape[2], A.shape[2], B.shape[1])
         self._packed = bytes(self._c)
+
+    A = property(lambda self: self._A)
+    B = property(lambda self: self._B)
+    scale = property(lambda self: self._scale)
+    n_groups = property(lambda self: self._n_groups)
+    out_features = property(lambda self: self._c.out)
 
 
 def lora_multi_workspace_size(X: torch.Tensor, W, bank: AdapterBank) -> int:
@@ -511,7 +519,7 @@ def lora_linear_fwd_multi(X: torch.Tensor, W, bias: Optional[torch.Tensor], bank
     if row_scale is not None and (row_scale.dtype is not torch.float32 or row_scale.numel() != T
                                   or not row_scale.is_contiguous()):
         raise ValueError("row_scale must be a contiguous float32 tensor with one entry per row of X")
-    device = _one_device("lora_linear_fwd_multi", X, W, bias, bank.A, slot, row_scale, out, workspace)
+    device = _one_device("lora_linear_fwd_multi", X, W, bias, bank._kept[0], slot, row_scale, out, workspace)
     if out is None:
         out = torch.empty(T, bank.out_features, dtype=out_dtype, device=X.device)
     lib = _load()
@@ -600,7 +608,7 @@ class Block8:
 
 
 class AdamWPlan:
-    """A prepared set of tensors (``lora_adamw_plan``); keeps the tensors and the device table."""
+    """A prepared set of tensors (``lora_adamw_plan``); keeps their memory and the device table."""
 
     def __init__(self, c: WpAdamWPlan, table: torch.Tensor, tensors, numels):
         self._table, self._tensors, self._numels = table, tensors, numels
@@ -612,12 +620,14 @@ def lora_adamw_plan(params: Sequence[torch.Tensor], m: Sequence, v: Sequence,
                     masters: Optional[Sequence[Optional[torch.Tensor]]] = None) -> AdamWPlan:
     """Prepare ``lora_adamw_step`` over ``params`` (bf16 or fp32, contiguous), their moments (fp32
     tensors, or ``Block8``) and, for bf16 parameters, optional fp32 masters that the step updates in
-    their place.  The plan refers to these tensors' memory: build it again when one is replaced."""
+    their place.  The plan keeps and updates the memory that these tensors have now: build it again when
+    one is given other memory (``p.data = ...``, ``Block8.codes = ...``)."""
     n = len(params)
     masters = list(masters) if masters is not None else [None] * n
     if not (n > 0 and n == len(m) == len(v) == len(masters)):
         raise ValueError("lora_adamw_plan: params, m, v and masters must be lists of one length")
     arr = (WpAdamWTensor * n)()
+    kept = []                                         # aliases: the table's addresses stay valid
     device = params[0].device
     for i, (p, mi, vi, ma) in enumerate(zip(params, m, v, masters)):
         numel, eight = p.numel(), isinstance(mi, Block8)
@@ -635,6 +645,7 @@ def lora_adamw_plan(params: Sequence[torch.Tensor], m: Sequence, v: Sequence,
                 raise ValueError(f"lora_adamw_plan: tensor {i}: a state of the wrong dtype, size, layout or device")
         if p.dtype not in _DT or not p.is_contiguous() or p.device != device:
             raise ValueError(f"lora_adamw_plan: parameter {i} must be contiguous bf16 or fp32 on {device}")
+        kept += [p.detach()] + [t.detach() for t, _, _ in parts]
         arr[i] = WpAdamWTensor(p.data_ptr(), None if ma is None else ma.data_ptr(), parts[0][0].data_ptr(),
                                parts[1][0].data_ptr(), parts[2][0].data_ptr() if eight else None,
                                parts[3][0].data_ptr() if eight else None, numel, _DT[p.dtype], 8 if eight else 32)
@@ -644,7 +655,7 @@ def lora_adamw_plan(params: Sequence[torch.Tensor], m: Sequence, v: Sequence,
     c = WpAdamWPlan()
     _check(lib.lora_adamw_plan_init(arr, n, table.data_ptr(), table.numel(), ctypes.byref(c), _stream(device)),
            "lora_adamw_plan")
-    return AdamWPlan(c, table, (list(params), list(m), list(v), masters), [p.numel() for p in params])
+    return AdamWPlan(c, table, kept, [p.numel() for p in params])
 
 
 def lora_adamw_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor]], lr: float, beta1: float = 0.9,
