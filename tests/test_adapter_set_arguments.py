@@ -1,5 +1,7 @@
 """Arguments of the adapter-set calls that a kernel could not use: refused on the host, before any
 pointer is passed on."""
+import ctypes
+
 import pytest
 import torch
 
@@ -109,3 +111,50 @@ def test_a_bank_keeps_the_memory_it_reads():
     scale.data, A.data, B.data = torch.zeros(2, device=DEV), torch.zeros_like(A), torch.zeros_like(B)
     fresh = [torch.full_like(t, float("nan")) for t in (A, B, scale) for _ in range(3)]
     assert torch.equal(wpg.lora_linear_fwd_multi(X, None, None, bank, slot), want) and len(fresh) == 9
+
+
+# ------------------------------------------------------------------------------ the C calls
+FAKE = 0x10000
+BF, F32, NF4 = wpg.WP_BF16, wpg.WP_FP32, wpg.WP_NF4
+ALIGN, SHAPE = -4, -2
+
+
+def _m(rows, cols, dtype=BF, data=FAKE, absmax=None, ld=None):
+    return wpg.WpMat(data, dtype, rows, cols, cols if ld is None else ld, absmax)
+
+
+def _o(rows, cols, dtype=BF, data=FAKE, ld=None):
+    return wpg.WpOut(data, dtype, rows, cols, cols if ld is None else ld)
+
+
+def _r(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def _multi(W=None, bias=None, scale=FAKE, slot=FAKE, row_scale=None):
+    bank = wpg.WpBank(FAKE, FAKE, scale, BF, 4, 1, 16, 128, 256)
+    return wpg.lib().lora_linear_fwd_multi(_r(_m(9, 128)), _r(W), _r(bias), _r(bank), slot, row_scale, 1.0, _r(_o(9, 256)),
+                                           FAKE, 1 << 40, None)
+
+
+def _norm_fwd(X=None, weight=None, bias=None, Y=None, stats=FAKE):
+    return wpg.lib().lora_norm_fwd(_r(X or _m(5, 64)), _r(weight), _r(bias), 0, 1e-5, _r(Y or _o(5, 64)), stats, None)
+
+
+def _norm_bwd(dY=None, X=None, weight=None, stats=FAKE, dX=None, dW=None, dB=None):
+    return wpg.lib().lora_norm_bwd(_r(dY or _m(5, 64)), _r(X or _m(5, 64)), _r(weight), stats, 0, _r(dX or _o(5, 64)),
+                                   _r(dW), _r(dB), FAKE, 1 << 30, None)
+
+
+def test_pointers_off_their_elements_boundary_are_refused():
+    assert _multi(bias=_m(1, 256, data=FAKE + 1)) == ALIGN and _multi(bias=_m(1, 256, F32, FAKE + 2)) == ALIGN
+    assert _multi(scale=FAKE + 2) == ALIGN and _multi(slot=FAKE + 1) == ALIGN and _multi(row_scale=FAKE + 2) == ALIGN
+    assert _multi(W=_m(256, 128, NF4, absmax=FAKE + 2)) == ALIGN
+    assert _norm_fwd(X=_m(5, 64, data=FAKE + 1)) == ALIGN and _norm_fwd(Y=_o(5, 64, data=FAKE + 1)) == ALIGN
+    assert _norm_fwd(X=_m(5, 64, F32, FAKE + 2), Y=_o(5, 64, F32)) == ALIGN
+    assert _norm_fwd(weight=_m(1, 64, data=FAKE + 1)) == ALIGN and _norm_fwd(bias=_m(1, 64, F32, FAKE + 2)) == ALIGN
+    assert _norm_fwd(stats=FAKE + 2) == ALIGN
+    assert _norm_bwd(dY=_m(5, 64, data=FAKE + 1)) == ALIGN and _norm_bwd(X=_m(5, 64, data=FAKE + 1)) == ALIGN
+    assert _norm_bwd(dX=_o(5, 64, data=FAKE + 1)) == ALIGN and _norm_bwd(weight=_m(1, 64, F32, FAKE + 2)) == ALIGN
+    assert _norm_bwd(stats=FAKE + 2) == ALIGN
+    assert _norm_bwd(dW=_o(1, 64, F32, FAKE + 2)) == ALIGN and _norm_bwd(dB=_o(1, 64, F32, FAKE + 1)) == ALIGN

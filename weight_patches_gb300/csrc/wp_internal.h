@@ -556,6 +556,13 @@ unsigned long long device_wait_limit_ns();
 // workspace bytes of lora_norm_bwd over [T, C]: a partial row of dw and db per CTA
 size_t norm_bwd_workspace(long long T, long long C, bool f32);
 
+// ------------------------------------------------------------------ checks of arguments
+// Whether an array of WP_BF16 or 4-byte elements starts on a boundary of theirs (null does): a kernel's
+// load from any other address faults.
+inline bool aligned_element(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == WP_BF16 ? 1u : 3u)) == 0;
+}
+
 // ------------------------------------------------------------------ NF4 table (host)
 void nf4_codebook_host(float out[16]);
 

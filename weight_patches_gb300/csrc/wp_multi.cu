@@ -119,6 +119,9 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
   if (!al16(X->data) || X->ld % 8 || !al16(bank->A) || !al16(bank->B)) return WP_ERR_ALIGN;
   if (W && (!al16(W->data) || W->ld % 8)) return WP_ERR_ALIGN;
   if (!al16(Y->data) || Y->ld % (Y->dtype == WP_BF16 ? 8 : 4)) return WP_ERR_ALIGN;
+  if ((bias && !aligned_element(bias->data, bias->dtype)) || (W && !aligned_element(W->absmax, WP_FP32)) ||
+      !aligned_element(bank->scale, WP_FP32) || !aligned_element(slot, WP_FP32) || !aligned_element(row_scale, WP_FP32))
+    return WP_ERR_ALIGN;
   Layout L = layout(X, W, bank);
   // a workspace sized for more rows may lack the partial sums of a few: those then go the way of many
   if (L.parts && workspace_bytes < L.total) {

@@ -1232,6 +1232,9 @@ int lora_norm_fwd(const wp_mat* X, const wp_mat* weight, const wp_mat* bias, int
   if (Y->rows != X->rows || Y->cols != X->cols) return WP_ERR_SHAPE;
   if (weight && !valid_vec(weight, X->cols)) return weight->data ? WP_ERR_SHAPE : WP_ERR_INVALID;
   if (bias && !valid_vec(bias, X->cols)) return bias->data ? WP_ERR_SHAPE : WP_ERR_INVALID;
+  if (!aligned_element(X->data, X->dtype) || !aligned_element(Y->data, Y->dtype) || !aligned_element(stats, WP_FP32) ||
+      (weight && !aligned_element(weight->data, weight->dtype)) || (bias && !aligned_element(bias->data, bias->dtype)))
+    return WP_ERR_ALIGN;
   if (X->cols > 0x3FFFFFFFLL || X->rows > 0x7FFFFFFFLL) return WP_ERR_UNSUPPORTED;
   if (X->rows == 0) return WP_OK;
   NormParams p{};
@@ -1274,7 +1277,11 @@ int lora_norm_bwd(const wp_mat* dY, const wp_mat* X, const wp_mat* weight, const
     if (!o->data) return WP_ERR_INVALID;
     if (o->dtype != WP_FP32) return WP_ERR_DTYPE;
     if (o->rows * o->cols != X->cols) return WP_ERR_SHAPE;
+    if (!aligned_element(o->data, WP_FP32)) return WP_ERR_ALIGN;
   }
+  if (!aligned_element(X->data, X->dtype) || !aligned_element(dY->data, dY->dtype) || !aligned_element(stats, WP_FP32) ||
+      (dX && !aligned_element(dX->data, dX->dtype)) || (weight && !aligned_element(weight->data, weight->dtype)))
+    return WP_ERR_ALIGN;
   if (X->cols > 0x3FFFFFFFLL || X->rows > 0x7FFFFFFFLL) return WP_ERR_UNSUPPORTED;
   const bool sums = dW || dB;
   const size_t need = sums ? norm_bwd_workspace(X->rows, X->cols, X->dtype == WP_FP32) : 0;
