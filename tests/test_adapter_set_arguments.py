@@ -158,3 +158,25 @@ def test_pointers_off_their_elements_boundary_are_refused():
     assert _norm_bwd(dX=_o(5, 64, data=FAKE + 1)) == ALIGN and _norm_bwd(weight=_m(1, 64, F32, FAKE + 2)) == ALIGN
     assert _norm_bwd(stats=FAKE + 2) == ALIGN
     assert _norm_bwd(dW=_o(1, 64, F32, FAKE + 2)) == ALIGN and _norm_bwd(dB=_o(1, 64, F32, FAKE + 1)) == ALIGN
+
+
+def test_a_vector_in_several_pieces_is_refused():
+    # as a matrix whose rows lie apart, or a column of one
+    assert _multi(bias=_m(2, 128, ld=136)) == SHAPE and _multi(bias=_m(256, 1, F32, ld=4)) == SHAPE
+    assert _norm_fwd(weight=_m(2, 32, ld=40)) == SHAPE and _norm_fwd(bias=_m(64, 1, ld=2)) == SHAPE
+    assert _norm_bwd(weight=_m(4, 16, F32, ld=24)) == SHAPE
+    assert _norm_bwd(dW=_o(2, 32, F32, ld=48)) == SHAPE and _norm_bwd(dB=_o(64, 1, F32, ld=3)) == SHAPE
+
+
+@pytest.mark.gpu
+def test_a_stacked_bias():
+    X, W = torch.randn(5, 64, device=DEV).bfloat16(), torch.randn(32, 64, device=DEV).bfloat16()
+    bank = wpg.AdapterBank(torch.zeros(1, 16, 64, device=DEV).bfloat16(), torch.zeros(1, 32, 8, device=DEV).bfloat16(),
+                           torch.ones(1, device=DEV), 2)
+    slot = torch.full((5,), -1, dtype=torch.int32, device=DEV)
+    wide = torch.randn(2, 24, device=DEV)
+    want = wpg.lora_linear_fwd_multi(X, W, wide[:, :16].reshape(-1), bank, slot)
+    assert torch.equal(wpg.lora_linear_fwd_multi(X, W, wide[:, :16].contiguous(), bank, slot), want)
+    for bias in (wide[:, :16], torch.randn(32, 3, device=DEV)[:, :1]):
+        with pytest.raises(wpg.WeightPatchesError, match="SHAPE"):
+            wpg.lora_linear_fwd_multi(X, W, bias, bank, slot)

@@ -562,6 +562,12 @@ size_t norm_bwd_workspace(long long T, long long C, bool f32);
 inline bool aligned_element(const void* p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == WP_BF16 ? 1u : 3u)) == 0;
 }
+// Whether a matrix that stands for a vector (a bias stacked [groups, out_g], say) lies in one piece, as the
+// kernels read it.
+template <typename M>
+bool one_piece(const M& m) {
+  return m.rows <= 1 || m.ld == m.cols;
+}
 
 // ------------------------------------------------------------------ NF4 table (host)
 void nf4_codebook_host(float out[16]);

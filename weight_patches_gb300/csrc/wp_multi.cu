@@ -111,7 +111,7 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
   if (!std::isfinite(rs)) return WP_ERR_INVALID;
   if (bias) {
     if (!bias->data || (bias->dtype != WP_BF16 && bias->dtype != WP_FP32)) return WP_ERR_INVALID;
-    if (bias->rows * bias->cols != bank->out) return WP_ERR_SHAPE;
+    if (bias->rows * bias->cols != bank->out || !one_piece(*bias)) return WP_ERR_SHAPE;
   }
   if (X->rows == 0) return WP_OK;
   if (!X->data || !Y->data || !bank->A || !bank->B || !bank->scale || !slot) return WP_ERR_INVALID;

@@ -1023,7 +1023,7 @@ int last_launch() {
 
 bool valid_vec(const wp_mat* v, long long C) {
   return v->data && (v->dtype == WP_BF16 || v->dtype == WP_FP32) && v->rows >= 1 && v->cols >= 1 &&
-         v->rows * v->cols == C;
+         v->rows * v->cols == C && one_piece(*v);
 }
 
 // How a row length is worked on: vectors (or single elements) per thread (0: the long form), rows
@@ -1276,7 +1276,7 @@ int lora_norm_bwd(const wp_mat* dY, const wp_mat* X, const wp_mat* weight, const
     if (!o) continue;
     if (!o->data) return WP_ERR_INVALID;
     if (o->dtype != WP_FP32) return WP_ERR_DTYPE;
-    if (o->rows * o->cols != X->cols) return WP_ERR_SHAPE;
+    if (o->rows * o->cols != X->cols || !one_piece(*o)) return WP_ERR_SHAPE;
     if (!aligned_element(o->data, WP_FP32)) return WP_ERR_ALIGN;
   }
   if (!aligned_element(X->data, X->dtype) || !aligned_element(dY->data, dY->dtype) || !aligned_element(stats, WP_FP32) ||
