@@ -538,7 +538,9 @@ int launch_multi_plan(const MultiCall& c, cudaStream_t stream);
 int launch_multi_shrink(const MultiCall& c, cudaStream_t stream);
 int multi_fused(const MultiCall& c, const wp_mat* W, cudaStream_t stream);   // wp_api.cu
 // Few rows (wp_multi_small.cu): H~ a (slot, 16 rank rows) per CTA, then W streamed once with the
-// rows as the MMA's width, K split over a cluster.
+// rows as the MMA's width, K split over a cluster.  At most kMultiFewRows: the first kernel lists a slot's
+// rows in shared memory.
+constexpr int kMultiFewRows = 256;
 bool multi_whole(const MultiCall& c);      // so few rows that the second kernel forms H~, too: no first one
 int launch_multi_shrink_small(const MultiCall& c, cudaStream_t stream);
 int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStream_t stream);

@@ -50,13 +50,16 @@ int check(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
 // 27-60 us on five layers (1536 -> 4608 and 8960, 4096^2, 5120^2, 8960 -> 1536; 8-16 slots in any order, in runs
 // or one) where the masked fused forward took 28-111; at 512 rows of one slot 28-69 against 29-66.
 constexpr int kSmallRows = 256;
+static_assert(kSmallRows <= kMultiFewRows, "the few-row kernels' lists");
 // Rows up to which a 4-bit weight takes the kernels that decode it into fragments: they decode it once per
 // 64 rows, the fused forward once per 512.  At 128 rows they took 24-140 us on nine layers (N 1536 to 28672,
 // K 1536 to 14336) where the fused forward took 44-176 and in no case 6% more; at 256 rows
 // 35-135 against 45-177 on the five with N <= 5120, too few column tiles to fill the fused forward's SMs,
 // but 60-287 against 45-142 on the others.
+constexpr int kNF4Rows = 128, kNF4RowsNarrow = 256, kNF4Narrow = 5120;
+static_assert(kNF4Rows <= kMultiFewRows && kNF4RowsNarrow <= kMultiFewRows, "the few-row kernels' lists");
 bool nf4_few(long long T, const wp_mat* W) {
-  return W && W->dtype == WP_NF4 && (T <= 128 || (T <= 256 && W->rows <= 5120));
+  return W && W->dtype == WP_NF4 && T <= (W->rows <= kNF4Narrow ? kNF4RowsNarrow : kNF4Rows);
 }
 bool small_rows(int T, const wp_mat* W) { return T <= kSmallRows && (!W || W->dtype == WP_BF16); }
 

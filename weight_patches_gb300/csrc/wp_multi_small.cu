@@ -34,7 +34,6 @@ namespace {
 
 constexpr int kShrinkThreads = 256;
 constexpr int kShrinkWarps = kShrinkThreads / 32;
-constexpr int kMaxSmallT = 1024;          // rows a call of these kernels may have
 
 // H~ of up to 8 NT rows (list[0 .. n)) for 16 rank rows, K split over the warps; the partial
 // sums go to red[warp][16][8 NT].  U: 32-wide k steps whose loads are issued together.
@@ -89,7 +88,7 @@ __device__ __forceinline__ void shrink_pass(const MultiCall& c, const uint16_t* 
 
 // Grid: (rows x parts, chunks of 16 rank rows), a cluster of `parts` CTAs per (row, chunk) sharing K.
 __global__ void __launch_bounds__(kShrinkThreads) multi_shrink_small_kernel(const MultiCall c, const int parts) {
-  __shared__ int list[kMaxSmallT];
+  __shared__ int list[kMultiFewRows];
   __shared__ int wcount[kShrinkWarps];
   __shared__ float red[kShrinkWarps * 16 * 32];
   __shared__ float sums[16 * 32];
@@ -179,7 +178,6 @@ constexpr int kSmallMaxStages = 8;
 struct SmallParams {
   MultiCall c;
   int has_w;
-  int whole;                   // H~ is formed here, too
   int tile;                    // rows of X per tile (128, or 64 where shared memory holds no more)
   int t16;                     // MMA width: rows of a tile rounded up to 16
   int splits, kb_per, k_blocks;
@@ -477,6 +475,7 @@ static int ranks_of_tile(const MultiCall& c) {
 bool multi_whole(const MultiCall& c) { return c.T <= 2 && c.T * ranks_of_tile(c) <= 64; }
 
 int launch_multi_shrink_small(const MultiCall& c, cudaStream_t stream) {
+  if (c.T > kMultiFewRows) return WP_ERR_UNSUPPORTED;
   // a sweep of a CTA's warps covers 1024 of K; up to four CTAs share a longer K while the grid stays
   // within eight CTAs per SM (most of a grid leaves at once where rows share slots)
   const int chunks = (c.G * c.R + 15) / 16;
@@ -512,7 +511,7 @@ int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStr
   SmallParams p{};
   p.c = c;
   p.has_w = W ? 1 : 0;
-  p.whole = multi_whole(c) ? 1 : 0;
+  const bool whole = multi_whole(c);       // H~ is formed here, too
   p.k_blocks = (c.K + kBK - 1) / kBK;
   const int n_tiles = (c.N + 127) / 128;
   int t_tiles = 0;
@@ -540,7 +539,7 @@ int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStr
     p.kb_per = (p.k_blocks + p.splits - 1) / p.splits;
     p.share = (tile + p.splits - 1) / p.splits;
     p.stage_bytes = kATileBytes + p.t16 * 128;
-    const int delta_bytes = p.whole ? c.T * (512 + ranks_of_tile(c) * 4) : p.share * 128 * 4;
+    const int delta_bytes = whole ? c.T * (512 + ranks_of_tile(c) * 4) : p.share * 128 * 4;
     p.stages = (kSmallSmem - 1024 - delta_bytes) / p.stage_bytes;
     if (p.stages > kSmallMaxStages) p.stages = kSmallMaxStages;
     if (p.stages > p.kb_per) p.stages = p.kb_per;
@@ -566,10 +565,10 @@ int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStr
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   // alone, the kernel starts after what came before it in the stream
-  cfg.attrs = p.whole ? attr + 1 : attr;
-  cfg.numAttrs = p.whole ? 1 : 2;
-  e = p.whole ? cudaLaunchKernelEx(&cfg, multi_small_kernel<true>, maps, p)
-              : cudaLaunchKernelEx(&cfg, multi_small_kernel<false>, maps, p);
+  cfg.attrs = whole ? attr + 1 : attr;
+  cfg.numAttrs = whole ? 1 : 2;
+  e = whole ? cudaLaunchKernelEx(&cfg, multi_small_kernel<true>, maps, p)
+            : cudaLaunchKernelEx(&cfg, multi_small_kernel<false>, maps, p);
   return e == cudaSuccess ? WP_OK : fail(e);
 }
 
