@@ -412,7 +412,7 @@ typedef struct wp_bank {
  * once to bf16 (one or two rows of few ranks keep it in fp32), sums are fp32 and the output is
  * rounded once.
  *   workspace: lora_multi_workspace_size(X, W, bank) bytes, 16-byte aligned; the size for more
- *   rows serves fewer, too (over a 4-bit weight perhaps by the kernels for many rows).
+ *   rows serves fewer, too, and a larger one changes nothing.
  * Alignment: as lora_linear_fwd's tensor-core path (16-byte bases and pitches, in % 8 == 0,
  * out_g % 8 == 0); n_groups <= 8.  Errors as lora_linear_fwd; WP_ERR_DTYPE for a bank that is
  * not bf16, WP_ERR_UNSUPPORTED for a rank above 256.

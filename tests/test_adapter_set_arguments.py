@@ -180,3 +180,44 @@ def test_a_stacked_bias():
     for bias in (wide[:, :16], torch.randn(32, 3, device=DEV)[:, :1]):
         with pytest.raises(wpg.WeightPatchesError, match="SHAPE"):
             wpg.lora_linear_fwd_multi(X, W, bias, bank, slot)
+
+
+# ------------------------------------------------------------------------------ workspace
+def _workspace(rows, K, N, G, R, slots, dtype):
+    W = None if dtype is None else _m(N, K, dtype, absmax=FAKE if dtype == NF4 else None)
+    bank = wpg.WpBank(FAKE, FAKE, FAKE, BF, slots, G, R, K, N)
+    return wpg.lib().lora_multi_workspace_size(_r(_m(rows, K)), _r(W), _r(bank))
+
+
+@pytest.mark.parametrize("dtype", [BF, NF4, None])
+@pytest.mark.parametrize("K,N,G,R,slots", [(4096, 28672, 2, 16, 16), (64, 8, 1, 8, 1), (1536, 4608, 3, 32, 8),
+                                           (5120, 5120, 1, 16, 64), (14336, 4096, 1, 16, 8), (8960, 5128, 1, 64, 300),
+                                           (65536, 1024, 1, 256, 4), (262144, 64, 1, 8, 2)])
+def test_the_workspace_for_more_rows_holds_fewer(K, N, G, R, slots, dtype):
+    sizes = [_workspace(T, K, N, G, R, slots, dtype) for T in list(range(1, 600)) + [2048, 32760]]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+    # and the call asks for no more than the size of its own rows
+    bank = wpg.WpBank(FAKE, FAKE, FAKE, BF, slots, G, R, K, N)
+    W = None if dtype is None else _m(N, K, dtype, absmax=FAKE if dtype == NF4 else None)
+    for T in (1, 7, 16, 64, 65, 97, 128, 129, 200, 256, 257, 500):
+        call = lambda nbytes: wpg.lib().lora_linear_fwd_multi(  # noqa: E731
+            _r(_m(T, K)), _r(W), None, _r(bank), FAKE, None, 1.0, _r(_o(T, N)), FAKE + 4, nbytes, None)
+        assert call(_workspace(T, K, N, G, R, slots, dtype)) == ALIGN       # (the workspace's own alignment: nothing runs)
+        assert call(64) == -5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,N", [(512, 5136), (4096, 1024)])
+@pytest.mark.parametrize("T", [1, 9, 40, 100, 128, 140])
+def test_a_workspace_for_more_rows_gives_the_same_bits(T, K, N):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    X = torch.randn(T, K, generator=g, device=DEV).bfloat16()
+    W = wpg.NF4Weight(torch.randint(0, 256, (N, K // 2), generator=g, device=DEV, dtype=torch.uint8),
+                      torch.rand(N * K // 64, generator=g, device=DEV), N, K)
+    bank = wpg.AdapterBank(torch.randn(3, 16, K, generator=g, device=DEV).bfloat16(),
+                           torch.randn(3, N, 16, generator=g, device=DEV).bfloat16(), torch.ones(3, device=DEV))
+    slot = torch.randint(-1, 3, (T,), generator=g, device=DEV, dtype=torch.int32)
+    size = wpg.lora_multi_workspace_size(torch.empty(2048, K, dtype=torch.bfloat16, device=DEV), W, bank)
+    want = wpg.lora_linear_fwd_multi(X, W, None, bank, slot)
+    got = wpg.lora_linear_fwd_multi(X, W, None, bank, slot, workspace=torch.empty(size, dtype=torch.uint8, device=DEV))
+    assert torch.equal(got, want)

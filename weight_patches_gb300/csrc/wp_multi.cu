@@ -58,9 +58,8 @@ static_assert(kSmallRows <= kMultiFewRows, "the few-row kernels' lists");
 // but 60-287 against 45-142 on the others.
 constexpr int kNF4Rows = 128, kNF4RowsNarrow = 256, kNF4Narrow = 5120;
 static_assert(kNF4Rows <= kMultiFewRows && kNF4RowsNarrow <= kMultiFewRows, "the few-row kernels' lists");
-bool nf4_few(long long T, const wp_mat* W) {
-  return W && W->dtype == WP_NF4 && T <= (W->rows <= kNF4Narrow ? kNF4RowsNarrow : kNF4Rows);
-}
+long long nf4_few_rows(const wp_mat* W) { return W->rows <= kNF4Narrow ? kNF4RowsNarrow : kNF4Rows; }
+bool nf4_few(long long T, const wp_mat* W) { return W && W->dtype == WP_NF4 && T <= nf4_few_rows(W); }
 bool small_rows(int T, const wp_mat* W) { return T <= kSmallRows && (!W || W->dtype == WP_BF16); }
 
 // H~ [T, G R16] | s [T] (many rows) | entries | their counts | rows with an adapter
@@ -99,7 +98,12 @@ extern "C" {
 
 size_t lora_multi_workspace_size(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
   if (check(X, W, bank) != WP_OK || X->rows == 0) return 0;
-  return layout(X, W, bank).total;
+  const Layout L = layout(X, W, bank);
+  if (!W || W->dtype != WP_NF4) return L.total;
+  // the partial sums of every call of at most these rows: a workspace for the largest batch serves them all
+  // by the same kernels
+  const long long few = nf4_few_rows(W) < X->rows ? nf4_few_rows(W) : X->rows;
+  return L.part + multi_nf4_most_sums(static_cast<int>(few), static_cast<int>(bank->out), static_cast<int>(bank->in)) * 4;
 }
 
 int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, const wp_bank* bank,
@@ -125,12 +129,7 @@ int lora_linear_fwd_multi(const wp_mat* X, const wp_mat* W, const wp_mat* bias, 
   if ((bias && !aligned_element(bias->data, bias->dtype)) || (W && !aligned_element(W->absmax, WP_FP32)) ||
       !aligned_element(bank->scale, WP_FP32) || !aligned_element(slot, WP_FP32) || !aligned_element(row_scale, WP_FP32))
     return WP_ERR_ALIGN;
-  Layout L = layout(X, W, bank);
-  // a workspace sized for more rows may lack the partial sums of a few: those then go the way of many
-  if (L.parts && workspace_bytes < L.total) {
-    L.parts = 0;
-    L.total = L.part;
-  }
+  const Layout L = layout(X, W, bank);
   if (!workspace || workspace_bytes < L.total) return WP_ERR_WORKSPACE;
   if (!al16(workspace)) return WP_ERR_ALIGN;
 

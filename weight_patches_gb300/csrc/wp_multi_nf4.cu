@@ -304,9 +304,9 @@ Cut cut_of(int T, int N, int K) {
   const int spans = (K + kSpan - 1) / kSpan, tiles = (N + 15) / 16;
   const int most = kMaxX / (c.nt * 8 * kSpan * 2);
   double least = 0;
-  for (int want = 1; want <= spans; ++want) {
-    const int per = (spans + want - 1) / want, n = (spans + per - 1) / per;
-    if (per > most || n != want) continue;
+  for (int per = std::min(most, spans); per >= 1; --per) {
+    const int n = (spans + per - 1) / per;
+    if ((spans + n - 1) / n != per) continue;        // n parts have fewer spans each
     const int ctas = device_sm_count() / (n * c.tiles);
     if (ctas < 1) break;
     const int round = ctas * kWarps, rounds = (tiles + round - 1) / round;
@@ -323,6 +323,19 @@ Cut cut_of(int T, int N, int K) {
 
 // Partial sums of the call's rows over the parts of K; 0 parts: K is too long for these kernels.
 int multi_nf4_parts(int T, int N, int K) { return cut_of(T, N, K).parts; }
+
+// Rows that are cut alike (as many tiles, as many 8-row tiles of them) differ in a part's price alone, which
+// grows with the rows: the first of such a stretch has the most parts, the last the most rows.
+size_t multi_nf4_most_sums(int T, int N, int K) {
+  size_t most = 0;
+  for (int t = 1; t <= T;) {
+    const Cut c = cut_of(t, N, K);
+    const int last = std::min(T, c.tiles * c.nt * 8);
+    most = std::max(most, static_cast<size_t>(c.parts) * last * N);
+    t = last + 1;
+  }
+  return most;
+}
 
 int launch_multi_nf4(const MultiCall& c, const void* codes, const float* absmax, float* part, int parts,
                      cudaStream_t stream) {
