@@ -547,7 +547,7 @@ int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStr
 // A few rows against a 4-bit weight (wp_multi_nf4.cu): H~ as above, partial sums over parts of K (0 parts:
 // K is too long), and their sum with the adapters' term.
 int multi_nf4_parts(int T, int N, int K);
-size_t multi_nf4_most_sums(int T, int N, int K);   // at least as many sums as any call of at most T rows has
+size_t multi_nf4_most_sums(int T, int N, int K);   // the sums of whichever call of at most T rows has the most
 int launch_multi_nf4(const MultiCall& c, const void* codes, const float* absmax, float* part, int parts,
                      cudaStream_t stream);
 

@@ -325,12 +325,20 @@ Cut cut_of(int T, int N, int K) {
 int multi_nf4_parts(int T, int N, int K) { return cut_of(T, N, K).parts; }
 
 // Rows that are cut alike (as many tiles, as many 8-row tiles of them) differ in a part's price alone, which
-// grows with the rows: the first of such a stretch has the most parts, the last the most rows.
+// grows with the rows: their parts only become fewer, and the last rows of each count have the most sums.
 size_t multi_nf4_most_sums(int T, int N, int K) {
   size_t most = 0;
   for (int t = 1; t <= T;) {
     const Cut c = cut_of(t, N, K);
-    const int last = std::min(T, c.tiles * c.nt * 8);
+    int last = std::min(T, c.tiles * c.nt * 8);
+    if (cut_of(last, N, K).parts != c.parts) {
+      int with = t;                       // has c.parts; `last` has fewer
+      while (last - with > 1) {
+        const int mid = (with + last) / 2;
+        (cut_of(mid, N, K).parts == c.parts ? with : last) = mid;
+      }
+      last = with;
+    }
     most = std::max(most, static_cast<size_t>(c.parts) * last * N);
     t = last + 1;
   }
