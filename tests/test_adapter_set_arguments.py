@@ -221,3 +221,15 @@ def test_a_workspace_for_more_rows_gives_the_same_bits(T, K, N):
     want = wpg.lora_linear_fwd_multi(X, W, None, bank, slot)
     got = wpg.lora_linear_fwd_multi(X, W, None, bank, slot, workspace=torch.empty(size, dtype=torch.uint8, device=DEV))
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------------------ sizes
+def test_sizes_beyond_the_kernels_32_bit_indexes_are_refused():
+    def multi(T, K, N):
+        bank = wpg.WpBank(FAKE, FAKE, FAKE, BF, 1, 1, 8, K, N)
+        return wpg.lib().lora_linear_fwd_multi(_r(_m(T, K)), _r(_m(N, K)), None, _r(bank), FAKE, None, 1.0,
+                                               _r(_o(T, N)), FAKE, 16, None)
+    # rows and columns are rounded up to tiles, K to the steps of a CTA's warps
+    for T, K, N in ((2 ** 31 - 1, 8, 8), (2 ** 31 - 256, 8, 8), (1, 2 ** 31 - 8, 8), (1, 2 ** 30, 8), (1, 8, 2 ** 31 - 8)):
+        assert multi(T, K, N) == -8, (T, K, N)
+    assert multi(2 ** 31 - 513, 8, 8) == multi(1, 2 ** 30 - 8, 8) == multi(1, 8, 2 ** 31 - 520) == -5

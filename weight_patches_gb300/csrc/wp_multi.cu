@@ -32,7 +32,9 @@ int check(const wp_mat* X, const wp_mat* W, const wp_bank* bank) {
   if (bank->in != X->cols || bank->out % bank->n_groups) return WP_ERR_SHAPE;
   if (bank->rank % 8) return WP_ERR_SHAPE;
   if (X->cols % 8 || (bank->out / bank->n_groups) % 8) return WP_ERR_ALIGN;
-  if (X->rows > 0x7FFFFFFFll || X->cols > 0x7FFFFFFFll || bank->out > 0x7FFFFFFFll) return WP_ERR_UNSUPPORTED;
+  // indexes are 32-bit: rows and columns are rounded up to tiles of 512 at most, and the warps of a CTA step
+  // through K some thousand at a time, past its end
+  if (X->rows > 0x7FFFFFFFll - 512 || X->cols > 0x3FFFFFFFll || bank->out > 0x7FFFFFFFll - 512) return WP_ERR_UNSUPPORTED;
   // the bank's rows are TMA coordinates
   if (bank->n_slots * bank->out > 0x7FFFFFFFll - 512 ||
       static_cast<long long>(bank->n_slots) * bank->n_groups * bank->rank > 0x7FFFFFFFll - 512)
