@@ -233,3 +233,10 @@ def test_sizes_beyond_the_kernels_32_bit_indexes_are_refused():
     for T, K, N in ((2 ** 31 - 1, 8, 8), (2 ** 31 - 256, 8, 8), (1, 2 ** 31 - 8, 8), (1, 2 ** 30, 8), (1, 8, 2 ** 31 - 8)):
         assert multi(T, K, N) == -8, (T, K, N)
     assert multi(2 ** 31 - 513, 8, 8) == multi(1, 2 ** 30 - 8, 8) == multi(1, 8, 2 ** 31 - 520) == -5
+
+
+def test_a_norm_takes_a_matrix():
+    with pytest.raises(ValueError, match="T, C"):
+        wpg.lora_norm_fwd(torch.zeros(64))
+    with pytest.raises(ValueError, match="T, C"):
+        wpg.lora_norm_bwd(torch.zeros(64), torch.zeros(64), None, torch.zeros(2, 1))

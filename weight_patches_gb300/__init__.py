@@ -540,6 +540,7 @@ def lora_norm_fwd(X: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
                   stats: Optional[torch.Tensor] = None):
     """y = (x - mu) r w + b over the rows of X [T, C] (kind ``WP_NORM_RMS``: mu = 0).  Returns
     (y, stats), stats [2, T] fp32 holding mu and r for ``lora_norm_bwd``."""
+    _check_rows(X)
     device = _one_device("lora_norm_fwd", X, weight, bias, out, stats)
     if out is None:
         out = torch.empty(X.shape, dtype=X.dtype, device=X.device)
@@ -562,6 +563,7 @@ def lora_norm_bwd(dY: torch.Tensor, X: torch.Tensor, weight: Optional[torch.Tens
                   kind: int = WP_NORM_LAYER, need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
                   workspace: Optional[torch.Tensor] = None):
     """(dX, dW, dB) of ``lora_norm_fwd`` from its stats; dW and dB fp32 [C], None where not asked for."""
+    _check_rows(X)
     T, C = X.shape
     _check_stats(stats, T)
     device = _one_device("lora_norm_bwd", X, dY, weight, stats, workspace)
@@ -585,6 +587,11 @@ def _pvec(t: Optional[torch.Tensor]) -> Optional[bytes]:
     if t is not None and t.dim() != 1:
         raise ValueError("weight and bias of a norm must be contiguous vectors")
     return _pmat(t)
+
+
+def _check_rows(X: torch.Tensor):
+    if X.dim() != 2:
+        raise ValueError("a norm's X must be a matrix [T, C]")
 
 
 def _check_stats(stats: torch.Tensor, T: int):
