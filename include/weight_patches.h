@@ -496,7 +496,8 @@ size_t lora_adamw_plan_size(const wp_adamw_tensor* tensors, int32_t n);
 
 /* Writes the set's table into `table` (16-byte aligned device memory of lora_adamw_plan_size
  * bytes, which has to live as long as the plan is used) with small kernels on `stream`, and
- * fills *plan.  At most 62400 tensors; every pointer aligned to its element type. */
+ * fills *plan.  At most 62400 tensors; every pointer aligned to its element type; no two arrays may
+ * overlap (a tensor listed twice would be updated by two CTAs at once: WP_ERR_INVALID). */
 int lora_adamw_plan_init(const wp_adamw_tensor* tensors, int32_t n, void* table, size_t table_bytes,
                          wp_adamw_plan* plan, void* stream);
 

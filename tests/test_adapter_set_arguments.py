@@ -240,3 +240,36 @@ def test_a_norm_takes_a_matrix():
         wpg.lora_norm_fwd(torch.zeros(64))
     with pytest.raises(ValueError, match="T, C"):
         wpg.lora_norm_bwd(torch.zeros(64), torch.zeros(64), None, torch.zeros(2, 1))
+
+
+# ------------------------------------------------------------------------------ AdamW's arrays
+def test_a_set_whose_arrays_overlap_is_refused():
+    def init(*tensors):
+        arr = (wpg.WpAdamWTensor * len(tensors))(*tensors)
+        return wpg.lib().lora_adamw_plan_init(arr, len(tensors), FAKE, 1 << 30, _r(wpg.WpAdamWPlan()), None)
+
+    def t(at, numel=1000, dtype=F32, bits=32, **kw):
+        a = dict(param=at, master=None, m=at + 0x100000, v=at + 0x200000, ms=at + 0x300000, vs=at + 0x400000)
+        a.update(kw)
+        return wpg.WpAdamWTensor(a["param"], a["master"], a["m"], a["v"], a["ms"], a["vs"], numel, dtype, bits)
+
+    a, far = 0x10000000, 0x20000000
+    assert init(t(a), t(a)) == -1                                     # listed twice
+    assert init(t(a), t(far), t(far + 0x800000, m=a + 0x100000)) == -1    # two tensors with one state
+    assert init(t(a, v=a + 0x100000)) == -1 and init(t(a, m=a + 3996)) == -1     # within one tensor; its last element
+    assert init(t(a, dtype=BF, master=a + 1996)) == -1
+    assert init(t(a, bits=8, m=a + 4000, v=a + 4999)) == -1
+    assert init(t(a, bits=8, ms=a + 0x200000)) == -1 and init(t(a, bits=8, ms=far, vs=far + 12)) == -1
+
+
+@pytest.mark.gpu
+def test_a_set_whose_arrays_only_touch():
+    # neighbours in one buffer; a tensor without elements may lie anywhere
+    buf, m, v = (torch.zeros(1002, device=DEV) for _ in range(3))
+    buf[:] = 1.0
+    cut = lambda x: [x[:500], x[500:500], x[500:501], x[501:]]  # noqa: E731
+    plan = wpg.lora_adamw_plan(cut(buf), cut(m), cut(v))
+    wpg.lora_adamw_step(plan, [torch.ones_like(x) for x in cut(buf)], 0.1, weight_decay=0.0)
+    assert (buf - 0.9).abs().max() < 1e-6
+    with pytest.raises(wpg.WeightPatchesError, match="INVALID"):
+        wpg.lora_adamw_plan([buf, buf[:10]], [m, torch.zeros(10, device=DEV)], [v, torch.zeros(10, device=DEV)])

@@ -16,6 +16,7 @@
 // steps near the top stay below 1.6 %.  The codes are those of the correctly rounded float32
 // sequence divide, root(s), multiply, round to even: an approximate quotient and root decide a
 // code wherever they lie clear of a rounding boundary, the exact sequence where they do not.
+#include <algorithm>
 #include <cmath>
 #include <new>
 #include <cstring>
@@ -492,6 +493,38 @@ int check_tensor(const wp_adamw_tensor& t) {
   return WP_OK;
 }
 
+// Whether every array of the set is memory of its own: a tensor listed twice (tied parameters) would be updated
+// by two CTAs at once.
+int check_apart(const wp_adamw_tensor* tensors, int n) {
+  struct Span {
+    uintptr_t from, to;
+  };
+  Span* spans = new (std::nothrow) Span[static_cast<size_t>(n) * 6];
+  if (!spans) return WP_ERR_INVALID;
+  int count = 0;
+  auto add = [&](const void* p, long long bytes) {
+    if (p) spans[count++] = Span{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(bytes)};
+  };
+  for (int i = 0; i < n; ++i) {
+    const wp_adamw_tensor& t = tensors[i];
+    if (t.numel == 0) continue;
+    const long long state = t.numel * (t.state_bits == 8 ? 1 : 4);
+    add(t.param, t.numel * (t.param_dtype == WP_BF16 ? 2 : 4));
+    add(t.master, t.numel * 4);
+    add(t.m, state);
+    add(t.v, state);
+    if (t.state_bits != 8) continue;
+    add(t.m_absmax, (t.numel + kBlock8 - 1) / kBlock8 * 4);
+    add(t.v_absmax, (t.numel + kBlock8 - 1) / kBlock8 * 4);
+  }
+  std::sort(spans, spans + count, [](const Span& a, const Span& b) { return a.from < b.from; });
+  int rc = WP_OK;
+  for (int i = 1; i < count && rc == WP_OK; ++i)
+    if (spans[i].from < spans[i - 1].to) rc = WP_ERR_INVALID;
+  delete[] spans;
+  return rc;
+}
+
 long long units_of(const wp_adamw_tensor& t) { return (t.numel + kUnit - 1) / kUnit; }
 
 int cuda_status(cudaError_t e) {
@@ -531,6 +564,8 @@ int lora_adamw_plan_init(const wp_adamw_tensor* tensors, int32_t n, void* table,
   }
   if (!table || table_bytes < lora_adamw_plan_size(tensors, n)) return WP_ERR_WORKSPACE;
   if (!al(table, 16)) return WP_ERR_ALIGN;
+  const int apart = check_apart(tensors, n);
+  if (apart != WP_OK) return apart;
   wp_adamw_plan out{};
   out.table = table;
   out.n_tensors = n;
