@@ -273,3 +273,14 @@ def test_a_set_whose_arrays_only_touch():
     assert (buf - 0.9).abs().max() < 1e-6
     with pytest.raises(wpg.WeightPatchesError, match="INVALID"):
         wpg.lora_adamw_plan([buf, buf[:10]], [m, torch.zeros(10, device=DEV)], [v, torch.zeros(10, device=DEV)])
+
+
+# ------------------------------------------------------------------------------ the one-adapter calls' bias
+def test_a_layers_bias_in_several_pieces_is_refused():
+    lib, X, W, Y = wpg.lib(), _m(9, 128), _m(256, 128), _o(9, 256)
+    ads = (wpg.WpAdapter * 2)(*[wpg.WpAdapter(_m(16, 128), _m(128, 16), 16.0, 1.0, None, 0) for _ in range(2)])
+    for bias in (_m(2, 128, ld=136), _m(256, 1, F32, ld=4)):
+        assert lib.lora_linear_fwd(_r(X), _r(W), _r(bias), None, 0, 1.0, _r(Y), FAKE, 1 << 40, None) == SHAPE
+        assert lib.lora_linear_fwd_grouped(_r(X), _r(W), _r(bias), 2, ads, 1.0, _r(Y), FAKE, 1 << 40, None) == SHAPE
+        out = wpg.WpOut(bias.data, bias.dtype, bias.rows, bias.cols, bias.ld)
+        assert lib.lora_merge(_r(W), _r(out), None, 0, 1.0, FAKE, 1 << 40, None) == SHAPE

@@ -514,7 +514,7 @@ int fwd_impl(const wp_mat* X, const wp_mat* W, const wp_mat* bias, int G, bool g
   if (W && W->dtype == WP_NF4 && w_mn && (N % 64 != 0 || W->ld != N)) return WP_ERR_SHAPE;
   if (bias) {
     if (!bias->data || (bias->dtype != WP_BF16 && bias->dtype != WP_FP32)) return WP_ERR_INVALID;
-    if (bias->rows * bias->cols != N) return WP_ERR_SHAPE;
+    if (bias->rows * bias->cols != N || !one_piece(*bias)) return WP_ERR_SHAPE;
   }
   if (T > 0x7FFFFFFFLL || K > 0x7FFFFFFFLL || N > 0x7FFFFFFFLL) return WP_ERR_UNSUPPORTED;
 
@@ -1679,7 +1679,7 @@ int merge_impl(const wp_mat* W, const wp_out* bias, const wp_adapter* ad, int n,
   if (bias) {
     if (!bias->data) return WP_ERR_INVALID;
     if (bias->dtype != WP_BF16 && bias->dtype != WP_FP32) return WP_ERR_DTYPE;
-    if (bias->rows * bias->cols != out) return WP_ERR_SHAPE;
+    if (bias->rows * bias->cols != out || !one_piece(*bias)) return WP_ERR_SHAPE;
   }
   float s_of[kMaxAd];
   BiasFoldParams fold{};                           // the adapters' legacy bias vectors
