@@ -489,8 +489,8 @@ class AdapterBank:
         if not A.device == B.device == scale.device:
             raise ValueError("AdapterBank tensors must be on one device")
         self._A, self._B, self._scale, self._n_groups = A, B, scale, n_groups
-        # aliases: the memory at the packed addresses lives as long as the bank does
-        self._kept = A.detach(), B.detach(), scale.detach()
+        # the memory at the packed addresses lives as long as the bank does
+        self._kept = A.untyped_storage(), B.untyped_storage(), scale.untyped_storage()
         self._c = WpBank(A.data_ptr(), B.data_ptr(), scale.data_ptr(), _DT[A.dtype], A.shape[0], n_groups,
                          B.shape[2], A.shape[2], B.shape[1])
         self._packed = bytes(self._c)
@@ -519,7 +519,7 @@ def lora_linear_fwd_multi(X: torch.Tensor, W, bias: Optional[torch.Tensor], bank
     if row_scale is not None and (row_scale.dtype is not torch.float32 or row_scale.numel() != T
                                   or not row_scale.is_contiguous()):
         raise ValueError("row_scale must be a contiguous float32 tensor with one entry per row of X")
-    device = _one_device("lora_linear_fwd_multi", X, W, bias, bank._kept[0], slot, row_scale, out, workspace)
+    device = _one_device("lora_linear_fwd_multi", X, W, bias, bank._A, slot, row_scale, out, workspace)
     if out is None:
         out = torch.empty(T, bank.out_features, dtype=out_dtype, device=X.device)
     lib = _load()
@@ -617,8 +617,8 @@ class Block8:
 class AdamWPlan:
     """A prepared set of tensors (``lora_adamw_plan``); keeps their memory and the device table."""
 
-    def __init__(self, c: WpAdamWPlan, table: torch.Tensor, tensors, numels):
-        self._table, self._tensors, self._numels = table, tensors, numels
+    def __init__(self, c: WpAdamWPlan, table: torch.Tensor, kept, numels):
+        self._table, self._kept, self._numels = table, kept, numels
         self._packed = bytes(c)
         self._pack_ptrs = struct.Struct(f"@{len(numels)}P").pack
 
@@ -634,7 +634,7 @@ def lora_adamw_plan(params: Sequence[torch.Tensor], m: Sequence, v: Sequence,
     if not (n > 0 and n == len(m) == len(v) == len(masters)):
         raise ValueError("lora_adamw_plan: params, m, v and masters must be lists of one length")
     arr = (WpAdamWTensor * n)()
-    kept = []                                         # aliases: the table's addresses stay valid
+    kept = []                                         # the memory behind the table's addresses
     device = params[0].device
     for i, (p, mi, vi, ma) in enumerate(zip(params, m, v, masters)):
         numel, eight = p.numel(), isinstance(mi, Block8)
@@ -652,7 +652,7 @@ def lora_adamw_plan(params: Sequence[torch.Tensor], m: Sequence, v: Sequence,
                 raise ValueError(f"lora_adamw_plan: tensor {i}: a state of the wrong dtype, size, layout or device")
         if p.dtype not in _DT or not p.is_contiguous() or p.device != device:
             raise ValueError(f"lora_adamw_plan: parameter {i} must be contiguous bf16 or fp32 on {device}")
-        kept += [p.detach()] + [t.detach() for t, _, _ in parts]
+        kept += [p.untyped_storage()] + [t.untyped_storage() for t, _, _ in parts]
         arr[i] = WpAdamWTensor(p.data_ptr(), None if ma is None else ma.data_ptr(), parts[0][0].data_ptr(),
                                parts[1][0].data_ptr(), parts[2][0].data_ptr() if eight else None,
                                parts[3][0].data_ptr() if eight else None, numel, _DT[p.dtype], 8 if eight else 32)
