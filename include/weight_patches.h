@@ -406,9 +406,11 @@ typedef struct wp_bank {
  *            replays of a captured graph.
  *   row_scale [T] fp32 on the device or NULL (1): the scale of each row's request.
  *   Y        [T, out] WP_BF16 or WP_FP32; must not overlap the inputs.
- * A row's result depends on that row and its adapter alone: a row without an adapter, or whose
- * s_t is exactly 0, equals the row of the plain projection, and values that are not finite in
- * one slot or row do not reach rows of other slots.  As in lora_linear_fwd, s X A^T is rounded
+ * A row's result is that row's and its adapter's: values that are not finite in one slot or row
+ * do not reach rows of other slots, and a row without an adapter, or whose s_t is exactly 0, is
+ * bit for bit the row that this call gives when no row of the batch has one.  The order of an
+ * adapted row's sums, and so its last bits, go by the batch as well (its rows, and how many of
+ * them share a slot); the same call gives the same bits.  As in lora_linear_fwd, s X A^T is rounded
  * once to bf16 (one or two rows of few ranks keep it in fp32), sums are fp32 and the output is
  * rounded once.
  *   workspace: lora_multi_workspace_size(X, W, bank) bytes, 16-byte aligned; the size for more
@@ -473,7 +475,7 @@ typedef struct wp_adamw_tensor {
   int32_t state_bits;
 } wp_adamw_tensor;
 
-/* A prepared set: filled by lora_adamw_plan; `table` is the caller's device memory. */
+/* A prepared set: filled by lora_adamw_plan_init; `table` is the caller's device memory. */
 enum { WP_ADAMW_MAX_LAUNCHES = 16, WP_ADAMW_TENSORS_PER_LAUNCH = 3900 };
 typedef struct wp_adamw_plan {
   void* table;
@@ -496,8 +498,9 @@ size_t lora_adamw_plan_size(const wp_adamw_tensor* tensors, int32_t n);
 
 /* Writes the set's table into `table` (16-byte aligned device memory of lora_adamw_plan_size
  * bytes, which has to live as long as the plan is used) with small kernels on `stream`, and
- * fills *plan.  At most 62400 tensors; every pointer aligned to its element type; no two arrays may
- * overlap (a tensor listed twice would be updated by two CTAs at once: WP_ERR_INVALID). */
+ * fills *plan; a step on another stream has to be ordered after them.  At most 62400 tensors; every
+ * pointer aligned to its element type; no two arrays may overlap (a tensor listed twice would be
+ * updated by two CTAs at once: WP_ERR_INVALID). */
 int lora_adamw_plan_init(const wp_adamw_tensor* tensors, int32_t n, void* table, size_t table_bytes,
                          wp_adamw_plan* plan, void* stream);
 
@@ -510,6 +513,8 @@ int lora_adamw_plan_init(const wp_adamw_tensor* tensors, int32_t n, void* table,
  * updated (8-bit moments are coded again after p has used them), each product and sum of m and v
  * a separate rounding.  A gradient that is not finite reaches its element's p, m and v, and every
  * value of its 8-bit block.
+ * The scalars travel with the launch: a captured graph replays the step number, rate and scale that it
+ * was captured with (only *grad_scale_dev is read anew), so a graph serves one step number.
  *   grads: host array of n_tensors device pointers, all of grad_dtype (WP_FP32 or WP_BF16); NULL
  *   leaves that tensor and its state untouched.  Read before the call returns.
  * Errors: WP_ERR_INVALID for a scalar that is not finite, betas outside [0, 1), eps < 0, step < 1.

@@ -670,7 +670,8 @@ def lora_adamw_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor]], lr
                     grad_scale: float = 1.0, grad_scale_tensor: Optional[torch.Tensor] = None) -> None:
     """One AdamW step, in place, over the plan's tensors.  ``grads``: one per tensor, contiguous, all
     fp32 or all bf16; None leaves its tensor untouched.  ``grad_scale_tensor``: a device fp32 scalar
-    that multiplies the gradients as well (a clip or loss scale)."""
+    that multiplies the gradients as well (a clip or loss scale).  A captured graph replays the ``lr``,
+    ``step`` and other numbers that it was captured with."""
     if len(grads) != len(plan._numels):
         raise ValueError("lora_adamw_step: one gradient (or None) per tensor")
     given = [g for g in grads if g is not None]

@@ -231,9 +231,11 @@ __device__ __forceinline__ float code_exact(float v, float top) {
 
 // Codes of this lane's 8 values in a block whose largest magnitude is top.  The estimate and the
 // exact sequence each differ from the real value by the roundings of a quotient, one or two roots
-// (the approximate root 2^-23) and a product: together below 4e-7 of the code, 5e-5 for m and 1e-4
-// for v.  A code further than that from a boundary between two codes is the exact sequence's; the
-// few others (one value in 8000, one in 4000) are formed again.
+// (the approximate root 2^-23), each halved by every root after it, and a product.  In units of 2^-24 of the
+// code, m: 1 + 2 + 1 and 0.5 + 1 + 1, together 3.9e-7, 5e-5 of a code at 127; v: 0.5 + 1 + 2 + 1 and
+// 0.25 + 0.5 + 1 + 1, together 4.4e-7, 1.11e-4 at 255.  A code further than that (6e-5, 1.2e-4) from a boundary
+// between two codes is the exact sequence's; the few others (one value in 8000, one in 4000) are
+// formed again.
 template <bool kSigned>
 __device__ __forceinline__ uint2 encode8(const F2 (&v)[4], float top) {
   // inside these limits the reciprocal is normal, and a share that the estimate takes as zero for
@@ -405,8 +407,10 @@ __device__ __forceinline__ void ask_ahead(const StepParams& p, uint2 unit, int l
 
 // A unit a CTA, a block of 256 elements a warp, four CTAs' loads in flight per SM.  kBits8: whether
 // the launch has 8-bit moments at all.  Measured over 57.6 million elements of 420 adapters, fp32
-// masters and gradients: 32-bit moments 237 us (6.8 TB/s, the copy rate); 8-bit 173 us, 1.03 GB at
-// 6.0 TB/s.  The 8-bit step is held back by its arithmetic (450 instructions per 8 elements, issue
+// gradients: 32-bit moments 237 us with fp32 parameters, 253 with bf16 ones and masters (6.8 TB/s, the copy
+// rate); 8-bit 172 us with bf16 parameters and masters, 1.04 GB at 6.1 TB/s, 159 with fp32 parameters (0.92 GB,
+// 5.8 TB/s).  With bf16 gradients, too, 167 us with masters (0.92 GB, 5.5 TB/s) and 149 without (0.58 GB, 3.9
+// TB/s): what is left is the 8-bit step's arithmetic.  The 8-bit step is held back by its arithmetic (450 instructions per 8 elements, issue
 // slots 54 % used) with the wait for loads behind it: without ask_ahead it takes 207 us; a persistent
 // grid that keeps the tensor's entry between units 227 us (more registers live, fewer loads in
 // flight), one that copies the next block through shared memory 238 us (its own 120 instructions).

@@ -10,7 +10,9 @@
 //           straight from global into mma.sync fragments -- the rank rows are the 16-row operand,
 //           the slot's rows of X the 8-wide one, both through the same permutation of k so that
 //           every lane loads 16 consecutive bytes -- and leave H~ = bf16(s X A^T).  mma.sync
-//           rather than tcgen05: there is no tile to keep, a row belongs to one slot only.
+//           rather than tcgen05: there is no tile to keep, a row belongs to one slot only.  bf16, as
+//           the operand of the second product (two pieces would double its work): it adds one to
+//           two percent to the error that rounding Y to bf16 makes.
 //           (One or two rows of few ranks do without: the main kernel forms their H~ from its part of K.)
 //   main    W^T tiles of 128 output columns as the M = 128 operand of tcgen05.mma and the rows of
 //           X (rounded up to 16) as its width, W and X by TMA.  K is split over a cluster of up to
@@ -524,7 +526,7 @@ int launch_multi_small(const MultiCall& c, const void* W, long long ldw, cudaStr
     p.tmem_cols = p.t16 <= 32 ? 32 : (p.t16 <= 64 ? 64 : 128);
     // K splits (a cluster's CTAs, up to 8, each with at least two K blocks): the count whose busiest
     // SM streams the least of K -- ceil(CTAs / SMs) / splits, the most splits on a tie.  Beyond 256
-    // CTAs the clusters no longer fit side by side: 64 rows of 5120 -> 5120 took 16.5 us with 6
+    // CTAs (of the 304 that 152 SMs hold) the clusters no longer fit side by side: 64 rows of 5120 -> 5120 took 16.5 us with 6
     // splits (240 CTAs), 22.6 with 7 (280) and 18.9 with 3 (120).
     const long long tiles = static_cast<long long>(n_tiles) * t_tiles;
     p.splits = 1;

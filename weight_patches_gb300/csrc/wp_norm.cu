@@ -27,6 +27,14 @@
 //   8000 x 4099 fp32    forward 93 us, 2.8 TB/s; backward 124 us, 3.2 TB/s
 // Shifted rows were read and written element by element first: 96 and 278 us, 102 and 161 us.  Their
 // backward takes half the rows a turn of an aligned one's: with as many, the registers spill.
+// The widest forms spill all the same (bytes a thread): the backward's of 32 elements 144 to 664 bf16, 192 to
+// 592 fp32, its shifted one of 24 120 to 288, the bf16 forward's of 32 72 to 208; others up to 48.
+//   8192 x 12288 bf16   forward 83 us, 4.8 TB/s; backward 137 us, 4.4 TB/s (24 elements a thread)
+//   8192 x 14336 bf16   forward 93 us, 5.0 TB/s; backward 203 us, 3.5 TB/s
+//   8192 x 12288 fp32   forward 277 us, 2.9 TB/s; backward 299 us, 4.0 TB/s
+// Rows beyond the registers of 512 threads (32768 columns of bf16 forward, 16384 of any other) or of which the
+// ring does not hold two turns (fp32 backward, from 13953 columns on) are read once per sum, element by
+// element: 2000 x 40000 bf16 forward 284 us, backward 961; fp32 392 and 1002, 8192 x 14336 fp32 backward 1032.
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -70,10 +78,6 @@ struct Raw {
     } else {
       u[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
     }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (uint32_t& w : u) w = 0;
   }
   __device__ __forceinline__ float at(int k) const {
     if constexpr (sizeof(T) == 4 || V == 1) return __uint_as_float(u[k]);
