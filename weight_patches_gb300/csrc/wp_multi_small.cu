@@ -11,8 +11,8 @@
 //           the slot's rows of X the 8-wide one, both through the same permutation of k so that
 //           every lane loads 16 consecutive bytes -- and leave H~ = bf16(s X A^T).  mma.sync
 //           rather than tcgen05: there is no tile to keep, a row belongs to one slot only.  bf16, as
-//           the operand of the second product (two pieces would double its work): it adds one to
-//           two percent to the error that rounding Y to bf16 makes.
+//           the operand of the second product (two pieces would double its work): 64 rows of rank 16
+//           are 0.3 % further from the 64-bit result than with H~ in fp32, Y's own rounding the rest.
 //           (One or two rows of few ranks do without: the main kernel forms their H~ from its part of K.)
 //   main    W^T tiles of 128 output columns as the M = 128 operand of tcgen05.mma and the rows of
 //           X (rounded up to 16) as its width, W and X by TMA.  K is split over a cluster of up to
