@@ -556,7 +556,10 @@ int lora_ce_fwd(const wp_mat* X, const wp_mat* W, const void* target, int32_t ta
  *   dX = G W,   dW = G^T X
  *   dX [T, K], dW [V, K], WP_BF16 or WP_FP32, either NULL: not wanted; overwritten (dW of no rows: zeros).
  * The logits are formed again, a piece of the vocabulary at a time; a row of G over its own 1 - p[target] is rounded
- * once to bf16 (the target's entry is then exact), sums are fp32, outputs are rounded once.  p is exp(z - lse) with the
+ * once to bf16 (the target's entry is then exact), whatever the outputs' types; sums are fp32, outputs are rounded once.
+ * dX takes the row's factor, dloss (1 - p[target]), in fp32.  dW takes it times X, in two bf16 parts (2^-16 of it is left)
+ * while at most 512 rows count; beyond, in one, so that each term of dW is rounded to bf16 a second time.  Rows that do
+ * not count change nothing in this.  p is exp(z - lse) with the
  * fp32 lse, so G's entries are off by up to about p 2^-23 (|lse| + 1) beyond that: a row whose target has all but some
  * 1e-6 of the probability has a gradient of that size and no digits.  The same call gives the same bits.  dloss and lse
  * of rows that do not count are not read into anything.

@@ -849,7 +849,8 @@ def lora_ce_bwd(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor, lse: tor
                 workspace: Optional[torch.Tensor] = None):
     """(dX, dW) of ``lora_ce_fwd`` from its lse and the gradient ``dloss`` [T] at the rows' losses (a mean
     over n rows: 1 / n each); None where not asked for.  G, the gradient at the logits, is rounded to
-    bf16 whatever the outputs' types."""
+    bf16 whatever the outputs' types; with more than 512 rows that count, so is X times each row's factor on its
+    way into dW."""
     _check_ce("lora_ce_bwd", X, target, lse, dloss)
     device = _one_device("lora_ce_bwd", X, W, target, lse, dloss, workspace)
     dx = torch.empty(X.shape, dtype=dX_dtype, device=X.device) if need_dX else None

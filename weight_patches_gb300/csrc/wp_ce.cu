@@ -50,6 +50,10 @@ constexpr int kCeSmem = 1024 + kCeStages * kCeStageBytes + 2 * kStgBytes + 256;
 // blocks 1.5e-7, 4.19 ms; 8 blocks 2.8e-7, 3.90 ms; 16 blocks 6.2e-7, 3.76 ms; in one piece 3.74 ms.
 constexpr int kCeChunk = 16;
 
+// Rows that count up to which Xs (see ce_pack_kernel) has two parts: dW's products twice, 8 blocks of 64 rows more beside
+// the K / 64 of every tile of G and dX.  Beyond, its one part rounds each term of dW a second time.
+constexpr int kCeTwoParts = 512;
+
 struct CeParams {
   const int* count;            // rows that count: n
   int mt, nt;                  // kCeDw: row tiles (of the vocabulary piece); column tiles
@@ -69,7 +73,7 @@ struct CeParams {
   const int* target;           // compact rows: y, and for kCeGrad the exponent's offset and the target's entry
   const float* lse2;
   const float* tval;
-  int lo;                      // kCeDw: X's second part follows this many rows on (0: it has none)
+  int lo;                      // kCeDw: X's second part, if the rows are few, follows this many rows on
   float* zt;                   // kCeLoss: log2 e times the target's logit
   float2* part;                // kCeLoss: [2 units of a row][rows]
   int ldpart;
@@ -127,7 +131,7 @@ struct CeWalk {
     groups_m = 1;
     if constexpr (kMode == kCeDw) {
       mb = p.mt;
-      kblocks = (n + kBK - 1) / kBK * (p.lo ? 2 : 1);
+      kblocks = (n + kBK - 1) / kBK * (n <= kCeTwoParts ? 2 : 1);
       units = mb * p.nt;
     } else if constexpr (kMode == kCeDx) {
       // as the first piece's, so that every piece adds to the planes that the first has written
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       const uint32_t full_l0 = mapa_shared(smem_u32(&full[0]), 0);
       CeWalk<kMode> walk(p, pair, npairs);
       CeFill f;
-      const int first_part = kMode == kCeDw && p.lo ? walk.kblocks / 2 : 0x7fffffff;
+      const int first_part = kMode == kCeDw && *p.count <= kCeTwoParts ? walk.kblocks / 2 : 0x7fffffff;
       while (ok && walk.next(p, f)) {
         const int a0 = f.m * kPairM + static_cast<int>(cta) * kBM;
         const int b0 = f.j * kBN + static_cast<int>(cta) * 128;
@@ -600,8 +604,8 @@ struct CePack {
   // backward
   const uint16_t* W; long long ldw;
   float* lse2_c; float* tval_c; float* rs_c;
-  uint16_t* Xs;                // [gk or 2 gk, K]: rs X in one bf16 part, or in two
-  int lo;                      // rows from the first part to the second (0: one)
+  uint16_t* Xs;                // [xs, K]: rs X in one bf16 part, or, of few rows that count, in two
+  int lo;                      // rows from the first part to the second
   float scale;
 };
 
@@ -618,7 +622,8 @@ constexpr float kCeLeast = 0x1p-20f;
 // Backward: a row of G is -dloss s (1 - p) at its target and dloss s p_v elsewhere, the p_v adding up to 1 - p.  Held
 // in bf16 its largest entry, the target's, would cost dX half a step of each row.  So G is kept divided by
 // rs = dloss s (1 - p), which makes that entry -1, exact, and rs goes to the other side: to dX's rows as they are
-// finished, in fp32, and for dW into X, Xs = rs X, in two bf16 parts while the rows are few and the second costs little.
+// finished, in fp32, and for dW into X, Xs = rs X, in two bf16 parts while the rows that count are few and the second
+// costs little.
 // p comes from the row's product with its target's row of W.
 template <bool kBack>
 __global__ void __launch_bounds__(256) ce_pack_kernel(const CePack p) {
@@ -649,6 +654,7 @@ __global__ void __launch_bounds__(256) ce_pack_kernel(const CePack p) {
     base += red[0][w];
     n += red[1][w];
   }
+  const bool two = n <= kCeTwoParts;            // Xs has its second part
   if (blockIdx.x == 0 && tid == 0) *p.count = n;
   const int vecs = p.K >> 3;
   for (int b0 = r0; b0 < min(p.T, r0 + p.rows); b0 += 64) {      // 64 rows at a time
@@ -723,7 +729,7 @@ __global__ void __launch_bounds__(256) ce_pack_kernel(const CePack p) {
             l[k] = pack_bf16x2(a0 - __uint_as_float(h[k] << 16), a1 - __uint_as_float(h[k] & 0xffff0000u));
           }
           hi[c] = make_uint4(h[0], h[1], h[2], h[3]);
-          if (p.lo) lo[c] = make_uint4(l[0], l[1], l[2], l[3]);
+          if (two) lo[c] = make_uint4(l[0], l[1], l[2], l[3]);
         }
       }
     }
@@ -734,7 +740,7 @@ __global__ void __launch_bounds__(256) ce_pack_kernel(const CePack p) {
     for (int r = n + static_cast<int>(blockIdx.x); r < end; r += gridDim.x)
       for (int c = tid; c < vecs; c += 256) {
         reinterpret_cast<uint4*>(p.Xs + static_cast<long long>(r) * p.K)[c] = make_uint4(0, 0, 0, 0);
-        if (p.lo) reinterpret_cast<uint4*>(p.Xs + (static_cast<long long>(r) + p.lo) * p.K)[c] = make_uint4(0, 0, 0, 0);
+        if (two) reinterpret_cast<uint4*>(p.Xs + (static_cast<long long>(r) + p.lo) * p.K)[c] = make_uint4(0, 0, 0, 0);
       }
   }
 }
@@ -1142,6 +1148,8 @@ struct CePlan {
   int run, parts;              // forward: tiles of a unit; parts of a row's sum
   int piece, pieces;           // backward: vocabulary columns at a time (a multiple of 256)
   int splits, gk;              // dX: most splits of a piece's contraction; G's rows (T rounded up to 64)
+  int lo;                      // dW: rows from Xs's first part to its second
+  long long xs;                // dW: rows of Xs
   long long plane;             // dX: rows of a split's plane
   size_t o_count, o_map, o_target, o_zt, o_lse2, o_tval, o_rs, o_x, o_xs, o_part, o_G, o_planes, total;
 };
@@ -1153,9 +1161,6 @@ constexpr long long kCePieceBytes = 256ll << 20;
 // Row blocks whose X is swept over the vocabulary together: their rows stay in L2 while W streams past once.
 constexpr long long kCeSweepBytes = 32ll << 20;
 constexpr int kCeMaxSplits = 16;
-// Rows up to which Xs has two parts: dW's products twice, 8 blocks of 64 rows more beside the K / 64 of every tile of G
-// and dX.
-constexpr int kCeTwoParts = 512;
 
 // Units of several tiles of one row block leave fewer parts to join, where there are tiles enough.
 int ce_run(long long mb, long long vt, int pairs) {
@@ -1220,7 +1225,9 @@ CePlan ce_plan(long long T, long long K, long long V, bool back) {
     q.o_tval = take(T * 4);
     q.o_rs = take(T * 4);
     q.o_x = take(T * K * 2);
-    q.o_xs = take(std::min<long long>(2 * q.gk, std::max(q.gk, 2 * kCeTwoParts)) * K * 2);
+    q.lo = std::min(q.gk, kCeTwoParts);
+    q.xs = std::max(q.gk, 2 * q.lo);           // of all rows one part, of few two
+    q.o_xs = take(q.xs * K * 2);
     const long long whole = 2ll * q.gk * q.vt * kBN;
     q.o_G = take(static_cast<size_t>(std::min(whole, std::max(kCePieceBytes, 2ll * q.gk * kBN))));
     // splits: up to 16 units a pair, and 16 in all
@@ -1531,7 +1538,7 @@ int lora_ce_bwd(const wp_mat* X, const wp_mat* W, const void* target, int32_t ta
   pk.tval_c = reinterpret_cast<float*>(ws + q.o_tval);
   pk.rs_c = reinterpret_cast<float*>(ws + q.o_rs);
   pk.Xs = dW ? reinterpret_cast<uint16_t*>(ws + q.o_xs) : nullptr;
-  pk.lo = q.T <= kCeTwoParts ? q.gk : 0;
+  pk.lo = q.lo;
   pk.scale = static_cast<float>(logit_scale);
 
   CeMaps grad{}, dx{}, dw{};
@@ -1545,7 +1552,7 @@ int lora_ce_bwd(const wp_mat* X, const wp_mat* W, const void* target, int32_t ta
   }
   if (dW) {
     if ((rc = map_bf16(&dw.a, G, q.piece, q.gk, q.piece, 64)) != WP_OK) return rc;
-    if ((rc = map_bf16(&dw.b, pk.Xs, q.K, q.gk + pk.lo, q.K, 64)) != WP_OK) return rc;
+    if ((rc = map_bf16(&dw.b, pk.Xs, q.K, q.xs, q.K, 64)) != WP_OK) return rc;
     rc = dW->dtype == WP_FP32 ? map_f32(&dw.y, dW->data, q.K, q.V, dW->ld) : map_bf16(&dw.y, dW->data, q.K, q.V, dW->ld, 128);
     if (rc != WP_OK) return rc;
   }
