@@ -545,7 +545,9 @@ int lora_rope(const wp_heads* Q, const wp_heads* K, const int32_t* positions, in
  *   loss, lse [T] fp32; either may be NULL.
  *   workspace: lora_ce_workspace_size(X, W, 0) bytes, 16-byte aligned; the size for more rows serves
  *   fewer, too, and a larger one changes nothing.  (No two calls that may run at once may share one.)
- * Products are exact and summed in fp32 (K in chunks that are added with rounding to nearest).
+ * Products are exact and summed in fp32: at most 1024 of them at a time on the tensor core, which cuts its sum every 16
+ * products, and these sums with rounding to nearest: a logit is within about 2^-20 of its terms' magnitudes, and half a
+ * step of fp32 for each further 1024 of K.
  */
 int lora_ce_fwd(const wp_mat* X, const wp_mat* W, const void* target, int32_t target_bits, double logit_scale,
                 float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream);
@@ -559,10 +561,11 @@ int lora_ce_fwd(const wp_mat* X, const wp_mat* W, const void* target, int32_t ta
  * once to bf16 (the target's entry is then exact), whatever the outputs' types; sums are fp32, outputs are rounded once.
  * dX takes the row's factor, dloss (1 - p[target]), in fp32.  dW takes it times X, in two bf16 parts (2^-16 of it is left)
  * while at most 512 rows count; beyond, in one, so that each term of dW is rounded to bf16 a second time.  Rows that do
- * not count change nothing in this.  p is exp(z - lse) with the
- * fp32 lse, so G's entries are off by up to about p 2^-23 (|lse| + 1) beyond that: a row whose target has all but some
- * 1e-6 of the probability has a gradient of that size and no digits.  The same call gives the same bits.  dloss and lse
- * of rows that do not count are not read into anything.
+ * not count change nothing in this.  Logits and both products are summed as the loss's logits, but 4096 products at a time:
+ * each is within about 2^-17 of its terms' magnitudes, and half a step for each further 4096.  p is exp(z - lse) with the fp32 lse, so G's entries
+ * are off by up to about p 2^-23 (|lse| + 1), and p times the logit's error, beyond their rounding: a row whose target has all
+ * but some 1e-6 of the probability has a gradient of that size and no digits.  The same call gives the same bits.  dloss
+ * and lse of rows that do not count are not read into anything.
  *   workspace: lora_ce_workspace_size(X, W, 1) bytes, 16-byte aligned, as above.
  */
 int lora_ce_bwd(const wp_mat* X, const wp_mat* W, const void* target, int32_t target_bits, const float* lse,

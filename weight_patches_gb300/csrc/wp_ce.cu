@@ -48,7 +48,13 @@ constexpr int kCeSmem = 1024 + kCeStages * kCeStageBytes + 2 * kStgBytes + 256;
 // in registers (rounding to nearest) while the next chunk runs in the other accumulator.  Off 64 bits (512 rows of 4096,
 // 32000 columns; in float32 products of another order 6.2e-7), and the time (6144 rows that count, 4096 x 131072): 4
 // blocks 1.5e-7, 4.19 ms; 8 blocks 2.8e-7, 3.90 ms; 16 blocks 6.2e-7, 3.76 ms; in one piece 3.74 ms.
-constexpr int kCeChunk = 16;
+//
+// The backward's logits and its products, dX's over the vocabulary and dW's over the rows, take 64 blocks at a time, cut 256 times,
+// for G is rounded to bf16 anyway.  (In one piece the error grows with the length: an entry of G of rows of 2^20 was 18 %
+// off, dW of 2^20 rows 3.7e-3.)  A sum's chunks are of equal length: a last one of two blocks would wait for the accumulator.
+// Time, 16 blocks, 64, in one piece: 2048 x 2048 x 65536 with dW 925, 898, 886 us; 4096 x 4096 x 131072, dX, 4210, 3990, 3987 us;
+// 64 rows with dW 565, 566, 626 us (the accumulator is free again before its sums are stored).
+constexpr int kCeChunk = 16, kCeSumChunk = 64;
 
 // Rows that count up to which Xs (see ce_pack_kernel) has two parts: dW's products twice, 8 blocks of 64 rows more beside
 // the K / 64 of every tile of G and dX.  Beyond, its one part rounds each term of dW a second time.
@@ -120,7 +126,9 @@ template <int kMode>
 struct CeWalk {
   int mb, units, groups_m;     // row tiles, units, row tiles swept together
   int u, step, kblocks;
-  int m, j, j1, split, kb;
+  int m, j, j1, split;
+  int kb0, kb, kb1;            // the tile's blocks, the next of them
+  int chunk = kCeChunk;        // at most so many a fill
   int splits, per;             // kCeDx
   __device__ __forceinline__ CeWalk(const CeParams& p, int pair, int npairs) {
     const int n = *p.count;
@@ -146,13 +154,12 @@ struct CeWalk {
       units = mb * ((p.nt + p.run - 1) / p.run);
     }
     j = j1 = 0;
-    kb = kblocks;
+    kb0 = kb = kb1 = 0;
     m = split = 0;
   }
   __device__ __forceinline__ bool next(const CeParams& p, CeFill& f) {
     bool open = false;
-    if (kb >= kblocks) {                       // the next tile
-      kb = 0;
+    if (kb >= kb1) {                           // the next tile
       if (kMode != kCeLoss || ++j >= j1) {     // the next unit
         u += step;
         if (u >= units) return false;
@@ -177,26 +184,22 @@ struct CeWalk {
           j1 = min(p.nt, j + p.run);
         }
       }
+      kb0 = kMode == kCeDx ? split * per : 0;
+      kb1 = kMode == kCeDx ? min(kblocks, kb0 + per) : kblocks;
+      if constexpr (kMode != kCeLoss) {
+        const int parts = (kb1 - kb0 + kCeSumChunk - 1) / kCeSumChunk;
+        chunk = parts > 1 ? (kb1 - kb0 + parts - 1) / parts : kCeSumChunk;
+      }
+      kb = kb0;
     }
     f.m = m;
     f.j = j;
     f.split = split;
-    f.first = kb == 0;
+    f.first = kb == kb0;
     f.open = open;
-    if constexpr (kMode == kCeDx) {
-      f.kb0 = split * per;
-      f.kb1 = min(kblocks, f.kb0 + per);
-      kb = kblocks;
-    } else if constexpr (kMode == kCeLoss) {
-      f.kb0 = kb;
-      f.kb1 = min(kblocks, kb + kCeChunk);
-      kb = f.kb1;
-    } else {
-      f.kb0 = 0;
-      f.kb1 = kblocks;
-      kb = max(kblocks, 1);                    // no rows at all: one fill without a block
-    }
-    f.last = kb >= kblocks;
+    f.kb0 = kb;
+    f.kb1 = kb = min(kb1, kb + chunk);      // (no rows at all, kCeDw: one fill without a block)
+    f.last = kb >= kb1;
     f.close = f.last && (kMode != kCeLoss || j + 1 >= j1);
     return true;
   }
@@ -279,9 +282,9 @@ __global__ void __launch_bounds__(kCeThreads, 1)
   grid_launch_dependents();                     // the next kernel's CTAs get ready as these end
   grid_dependency_wait();                       // the rows, their number and G come from earlier kernels
 
-  // kCeLoss holds a row's 128 logits in registers: of the 384 x 168 that the block is launched with, the first
+  // the epilogue holds a row's 128 sums in registers: of the 384 x 168 that the block is launched with, the first
   // warpgroup keeps 56 each and the epilogue's two get 224
-  if (kMode == kCeLoss && warp < kCeEpi0) regs_dec<56>();
+  if (warp < kCeEpi0) regs_dec<56>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
     if (lane == 0) {
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     }
   } else if (warp >= kCeEpi0) {
     // ------------------------------------------------------------ epilogue
-    if (kMode == kCeLoss) regs_inc<224>();
+    regs_inc<224>();
     // a thread is a row of the CTA's 128 and one half (eg) of the tile's 256 columns
     const int eg = (warp - kCeEpi0) >> 2;
     const int q = warp & 3;                      // the tensor-memory lanes that this warp may read
@@ -411,8 +414,31 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       staged = true;
     };
 
+    float z[128];                                // the row's sums over this half tile
+    // adds a chunk to them
+    auto gather = [&](const CeFill& f) {
+      const uint32_t t0 = tmem + (count & 1) * kBN + lane_base + eg * 128;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r[32], q[32];
+        tmem_ld32x2(t0 + c * 64, r, t0 + c * 64 + 32, q);
+        if (f.first) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            z[c * 64 + i] = __uint_as_float(r[i]);
+            z[c * 64 + 32 + i] = __uint_as_float(q[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            z[c * 64 + i] += __uint_as_float(r[i]);
+            z[c * 64 + 32 + i] += __uint_as_float(q[i]);
+          }
+        }
+      }
+      release_acc();
+    };
     if constexpr (kMode == kCeLoss) {
-      float z[128];                              // the row's logits of this half tile
       float top = -INFINITY, sum = 0.f;          // running maximum and sum, base 2
       int target = -1;
       while (walk.next(p, f)) {
@@ -427,26 +453,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         const bool okw = mbar_wait(&acc_full[count & 1], static_cast<uint32_t>(count >> 1) & 1u, abort_flag, tmo, status);
         if (!__all_sync(0xffffffffu, okw)) break;
         tc_fence_after();
-        const uint32_t t0 = tmem + (count & 1) * kBN + lane_base + eg * 128;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t r[32], q[32];
-          tmem_ld32x2(t0 + c * 64, r, t0 + c * 64 + 32, q);
-          if (f.first) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              z[c * 64 + i] = __uint_as_float(r[i]);
-              z[c * 64 + 32 + i] = __uint_as_float(q[i]);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              z[c * 64 + i] += __uint_as_float(r[i]);
-              z[c * 64 + 32 + i] += __uint_as_float(q[i]);
-            }
-          }
-        }
-        release_acc();
+        gather(f);
         if (!f.last) continue;
         const int col = f.j * kBN + eg * 128;
         const int cols = p.V - col;              // columns of the vocabulary from here
@@ -478,28 +485,31 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         if (f.close && row_ok) p.part[static_cast<long long>(f.j / p.run * 2 + eg) * p.ldpart + row] = make_float2(top, sum);
       }
     } else if constexpr (kMode == kCeGrad) {
+      int target = -1;
+      float lse2 = 0.f, tval = 0.f;
       while (walk.next(p, f)) {
         const int row0 = f.m * kPairM + static_cast<int>(cta) * kBM;
         const int row = row0 + row_in_cta;
         const bool row_ok = row < n;
-        const int target = row_ok ? p.target[row] : -1;
-        const float lse2 = row_ok ? p.lse2[row] : 0.f, tval = row_ok ? p.tval[row] : 0.f;
+        if (f.first) {
+          target = row_ok ? p.target[row] : -1;
+          lse2 = row_ok ? p.lse2[row] : 0.f;
+          tval = row_ok ? p.tval[row] : 0.f;
+        }
         if (!wait_acc()) break;
-        const uint32_t t0 = tmem + (count & 1) * kBN + lane_base + eg * 128;
+        gather(f);
+        if (!f.last) continue;
         const int pcol = f.j * kBN + eg * 128;   // column within the piece
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 2; ++c) {            // 64 columns to a 128-byte row of the staging buffer
           stg_free();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t r[32];
-            tmem_ld32(t0 + c * 64 + h * 32, r);
-            if (c == 1 && h == 1) release_acc();
             const int col = p.v0 + pcol + c * 64 + h * 32;
             const int at = target - col, cols = p.V - col;
             float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(__uint_as_float(r[i]), p.c2, -lse2));
+            for (int i = 0; i < 32; ++i) v[i] = ex2(fmaf(z[c * 64 + h * 32 + i], p.c2, -lse2));
             if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
@@ -527,50 +537,61 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       }
       if (elected) bulk_wait_all();
     } else {
-      const bool f32 = kMode == kCeDx || p.out_f32;
-      const int cw = f32 ? 32 : 64;              // columns per 128-byte row of the staging buffer
-      while (walk.next(p, f)) {
-        const bool some = f.kb1 > f.kb0;
-        if (some && !wait_acc()) break;
-        const uint32_t t0 = tmem + (count & 1) * kBN + lane_base + eg * 128;
-        const int col0 = f.j * kBN + eg * 128;
+      // the staging buffer's 128-byte rows to the tile's columns from c on
+      auto store = [&](const CeFill& f, int c) {
+        fence_proxy_async_smem();
+        named_bar_sync(bar_main, 128);
+        const int col = f.j * kBN + eg * 128 + c;
         const int row0 = f.m * kPairM + static_cast<int>(cta) * kBM;
-        const int yrow = kMode == kCeDx ? f.split * p.plane + row0 : p.v0 + row0;
         const bool rows = kMode == kCeDx ? row0 < n : p.v0 + row0 < p.V;
-        const int chunks = 128 / cw;
+        if (elected && rows && col < p.K) {
+          const int yrow = kMode == kCeDx ? f.split * p.plane + row0 : p.v0 + row0;
+          if (kMode == kCeDx && p.add)
+            tma_add_2d(&maps.y, col, yrow, buf);
+          else
+            tma_store_2d(&maps.y, col, yrow, buf);
+          bulk_commit();
+        }
+      };
+      const bool f32 = kMode == kCeDx || p.out_f32;
+      while (walk.next(p, f)) {
+        if (kMode == kCeDw && n == 0) {          // no row counts, no fill has a block
+          const int cw = f32 ? 32 : 64;
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          stg_free();
-#pragma unroll 1
-          for (int h = 0; h < cw / 32; ++h) {
-            uint32_t r[32];
-            if (some) {
-              tmem_ld32(t0 + c * cw + h * 32, r);
-              if (c == chunks - 1 && h == cw / 32 - 1) release_acc();
-            } else {
+          for (int c = 0; c < 128; c += cw) {
+            stg_free();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = 0u;
-            }
-            if (f32) {
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                st_shared_v4(rowb + ((u ^ (row_in_cta & 7)) * 16), r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
-            } else {
-              auto pk = [&](int i) { return pack_bf16x2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])); };
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                st_shared_v4(rowb + (((h * 4 + u) ^ (row_in_cta & 7)) * 16), pk(8 * u), pk(8 * u + 2), pk(8 * u + 4),
-                             pk(8 * u + 6));
-            }
+            for (int u = 0; u < 8; ++u) st_shared_v4(rowb + u * 16, 0u, 0u, 0u, 0u);
+            store(f, c);
           }
-          fence_proxy_async_smem();
-          named_bar_sync(bar_main, 128);
-          if (elected && rows && col0 + c * cw < p.K) {
-            if (kMode == kCeDx && p.add)
-              tma_add_2d(&maps.y, col0 + c * cw, yrow, buf);
-            else
-              tma_store_2d(&maps.y, col0 + c * cw, yrow, buf);
-            bulk_commit();
+          continue;
+        }
+        if (!wait_acc()) break;
+        gather(f);
+        if (!f.last) continue;
+        if (f32) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            stg_free();
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int i = c * 32 + 4 * u;
+              st_shared_v4(rowb + ((u ^ (row_in_cta & 7)) * 16), __float_as_uint(z[i]), __float_as_uint(z[i + 1]),
+                           __float_as_uint(z[i + 2]), __float_as_uint(z[i + 3]));
+            }
+            store(f, c * 32);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            stg_free();
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int i = c * 64 + 8 * u;
+              st_shared_v4(rowb + ((u ^ (row_in_cta & 7)) * 16), pack_bf16x2(z[i], z[i + 1]), pack_bf16x2(z[i + 2], z[i + 3]),
+                           pack_bf16x2(z[i + 4], z[i + 5]), pack_bf16x2(z[i + 6], z[i + 7]));
+            }
+            store(f, c * 64);
           }
         }
       }
