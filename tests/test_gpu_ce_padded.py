@@ -28,3 +28,16 @@ def test_rows_that_do_not_count_leave_dw_as_it_is(T, n):
         assert torch.equal(got, want)
     torch.cuda.synchronize()
     assert wpg.lora_device_status() == 0
+
+
+def test_one_row_of_a_short_pitch():
+    # the transpose of a column: strides (1, 1)
+    x, w, y = case(1, 512, 40)
+    col = torch.empty(512, 1, dtype=torch.bfloat16, device=DEV).t()
+    col.copy_(x)
+    assert col.stride() == (1, 1)
+    d = torch.ones(1, device=DEV)
+    a, b = wpg.lora_ce_fwd(x, w, y), wpg.lora_ce_fwd(col, w, y)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    a, b = wpg.lora_ce_bwd(x, w, y, a[1], d), wpg.lora_ce_bwd(col, w, y, a[1], d)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])

@@ -260,6 +260,11 @@ def _pout(t: torch.Tensor) -> bytes:
     return _pmat(t)[:40]                          # wp_out: wp_mat without its last pointer
 
 
+def _sized(t: torch.Tensor):
+    """The matrix as _pmat passes it to a call, for the size of that call's workspace."""
+    return _ref(WpMat.from_buffer_copy(_pmat(t)))
+
+
 def _one_device(call: str, first: torch.Tensor, *others) -> int:
     """The index of the CUDA device that all of a call's tensors lie on (None: an argument not given).
     A kernel would read a host pointer as its own memory."""
@@ -691,7 +696,7 @@ def lora_residual_norm_fwd(X: torch.Tensor, Y: Optional[torch.Tensor] = None, ga
 
 
 def lora_residual_norm_bwd_workspace_size(X1: torch.Tensor) -> int:
-    return _load().lora_workspace_size(WP_OP_RESIDUAL_NORM_BWD, _ref(_mat(X1)), None, None, 0)
+    return _load().lora_workspace_size(WP_OP_RESIDUAL_NORM_BWD, _sized(X1), None, None, 0)
 
 
 def lora_residual_norm_bwd(dH: torch.Tensor, X1: torch.Tensor, stats: torch.Tensor, Y: Optional[torch.Tensor] = None,
@@ -811,7 +816,7 @@ def lora_rope_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", s
 
 # ------------------------------------------------------------------------------------ loss
 def lora_ce_workspace_size(X: torch.Tensor, W: torch.Tensor, backward: bool = False) -> int:
-    return _load().lora_ce_workspace_size(_ref(_mat(X)), _ref(_mat(W)), 1 if backward else 0)
+    return _load().lora_ce_workspace_size(_sized(X), _sized(W), 1 if backward else 0)
 
 
 def _check_ce(call: str, X: torch.Tensor, target: torch.Tensor, *rows) -> None:

@@ -1385,7 +1385,7 @@ int ce_zero(const wp_out* o, cudaStream_t st) {
 // A matrix of one row has no pitch that could be off.
 template <typename M>
 const M* one_row(const M* m, M* own) {
-  if (!m || m->rows != 1 || m->ld <= m->cols) return m;
+  if (!m || m->rows != 1) return m;
   *own = *m;
   own->ld = m->cols;
   return own;
