@@ -481,7 +481,8 @@ typedef struct wp_residual_norm {
  *   stats [4, T] fp32 or NULL: mean and factor of norm2, then (rows 2 and 3, with a post norm only) of norm1.
  * C <= 16384, T < 2^30, any pitch; 16-byte aligned rows are fastest.  Sums are fp32, means taken out before squaring;
  * h is formed from x1 before its rounding to X_out's type; one rounding per output.  The order of a row's sums, and so
- * the last bits, go by the rows' length, types and alignment, not by their number; the same call gives the same bits.
+ * the last bits, go by the rows' length and types and by the addresses' and pitches' alignment, not by the rows' number; the
+ * same call gives the same bits.
  */
 int lora_residual_norm_fwd(const wp_mat* X, const wp_mat* Y, const wp_residual_norm* a, const wp_out* X_out,
                            const wp_out* H, float* stats, void* stream);

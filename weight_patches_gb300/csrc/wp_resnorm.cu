@@ -1063,7 +1063,8 @@ int rn_common(const wp_mat* X, const wp_mat* Y, const wp_residual_norm* a, RnPar
   return WP_OK;
 }
 
-// A further matrix of the rows' sizes: its type, sizes and alignment, and whether 16-byte pieces fit it.
+// A further matrix of the rows' sizes: its type, sizes and alignment, and whether 16-byte pieces fit it.  (The pitch decides for
+// one row, too: the pieces order a row's sums, and the same row has the same bits alone and among others.)
 template <typename M>
 int rn_rows(const M* m, const RnParams& p, int dtype, bool* vec) {
   if (!m) return WP_OK;
@@ -1071,7 +1072,7 @@ int rn_rows(const M* m, const RnParams& p, int dtype, bool* vec) {
   if (m->dtype != dtype) return WP_ERR_DTYPE;
   if (m->rows != p.T || m->cols != p.C) return WP_ERR_SHAPE;
   if (!aligned_element(m->data, m->dtype)) return WP_ERR_ALIGN;
-  *vec = *vec && al16(m->data) && (p.T == 1 || m->ld % (dtype == WP_FP32 ? 4 : 8) == 0);
+  *vec = *vec && al16(m->data) && m->ld % (dtype == WP_FP32 ? 4 : 8) == 0;
   return WP_OK;
 }
 
