@@ -24,7 +24,7 @@ thread_local std::string g_last_error;
 
 // How long a bounded device wait spins before its kernel gives up (lora_set_wait_limit), and
 // the test hook that holds the fused forward's row-block flags one release short and keeps
-// the one-pass 4-bit merge's last MMAs back (lora_debug_hold_flags).
+// the one-pass 4-bit merge's last MMAs and the residual norm's rows back (lora_debug_hold_flags).
 std::atomic<unsigned long long> g_wait_limit_ns{2000000000ull};
 std::atomic<int> g_hold_flags{0};
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
@@ -145,6 +145,7 @@ int encode_map(CUtensorMap* m, int dtype, const void* ptr, long long inner, long
   return make_map(m, dtype, ptr, inner, outer, ld, box_inner, box_outer, swizzle);
 }
 unsigned long long device_wait_limit_ns() { return wait_limit_ns(); }
+int debug_hold_flags() { return g_hold_flags.load(); }
 
 namespace {
 

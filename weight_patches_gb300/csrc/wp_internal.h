@@ -556,6 +556,7 @@ int encode_map_bf16(CUtensorMap* m, const void* ptr, long long inner, long long 
 int encode_map(CUtensorMap* m, int dtype, const void* ptr, long long inner, long long outer, long long ld, int box_inner,
                int box_outer, int swizzle);   // dtype WP_BF16 or WP_FP32
 unsigned long long device_wait_limit_ns();
+int debug_hold_flags();          // whether lora_debug_hold_flags is on
 
 // ------------------------------------------------------------------ norms
 // workspace bytes of lora_norm_bwd over [T, C]: a partial row of dw and db per CTA

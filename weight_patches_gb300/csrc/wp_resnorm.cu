@@ -94,6 +94,7 @@ struct RnParams {
   int stages, slot;                            // the ring: rows ahead, bytes of one
   int* status;
   unsigned long long timeout_ns;
+  int hold;                                    // test hook: no row is sent for, the first wait runs out
   int out_vec;                                 // 16-byte stores fit the outputs below
   float* out[4];                               // dgate, dmul, dadd, dw1
   float* part[4];                              // [workers][2][C] each
@@ -266,8 +267,9 @@ struct Ring {
     }
     __syncthreads();
   }
+  // (a warp's lanes go on or leave together: shuffles follow)
   __device__ __forceinline__ bool wait(const RnParams& p) {
-    return mbar_wait(&full[turn], phase, abort_flag, p.timeout_ns, p.status);
+    return __all_sync(0xffffffffu, mbar_wait(&full[turn], phase, abort_flag, p.timeout_ns, p.status));
   }
   __device__ __forceinline__ const uint8_t* row(const RnParams& p) const { return slots + turn * p.slot; }
   __device__ __forceinline__ void next(const RnParams& p) {
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, kMin) resnorm_fwd_kernel(const __gri
   }
   if (kRing) {
     if (threadIdx.x == 0)
-      for (int i = 0; i < p.stages && r0 + i * rs < r1; ++i) issue(r0 + i * rs, i);
+      for (int i = 0; i < p.stages && r0 + i * rs < r1 && !p.hold; ++i) issue(r0 + i * rs, i);
   } else {
 #pragma unroll
     for (int j = 0; j < NA; ++j) {
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, kMin) resnorm_bwd_kernel(const __gri
   }
   if (kRing) {
     if (threadIdx.x == 0)
-      for (int i = 0; i < p.stages && r0 + i < r1; ++i) issue(r0 + i, i);
+      for (int i = 0; i < p.stages && r0 + i < r1 && !p.hold; ++i) issue(r0 + i, i);
   }
   if constexpr (!kRing) {
 #pragma unroll
@@ -1119,6 +1121,7 @@ int lora_residual_norm_fwd(const wp_mat* X, const wp_mat* Y, const wp_residual_n
   p.mod_per = static_cast<int>(p.T / std::max(1ll, mod_n));
   p.stats = stats;
   p.timeout_ns = device_wait_limit_ns();
+  p.hold = debug_hold_flags();
   if (!(p.status = tc_status_ptr())) {
     set_last_cuda_error(cudaGetLastError());
     return WP_ERR_CUDA;
@@ -1192,6 +1195,7 @@ int lora_residual_norm_bwd(const wp_mat* dH, const wp_mat* dX1, const wp_mat* X1
   p.mod_per = static_cast<int>(p.T / std::max(1ll, mod_n));
   p.stats_in = stats;
   p.timeout_ns = device_wait_limit_ns();
+  p.hold = debug_hold_flags();
   if (!(p.status = tc_status_ptr())) {
     set_last_cuda_error(cudaGetLastError());
     return WP_ERR_CUDA;
