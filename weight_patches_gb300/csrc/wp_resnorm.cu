@@ -973,7 +973,7 @@ int rn_launch(RnParams& p, cudaStream_t st) {
   const bool pair = !kBack && s.form == kRnPairFwd && !s.warp;
   if constexpr (!kBack)
     if (pair) WP_RN(false, 2, kRnPairFwd, 2, 1);
-  constexpr bool kHalf = !kBack || (!kPost && sizeof(TS) == 2);
+  constexpr bool kHalf = !kBack || (!kPost && sizeof(TS) == 2);   // as rn_shape has it
   const bool half = kHalf && s.form == kRnHalf && s.pieces == 2;
   if constexpr (kHalf)
     if (half) WP_RN(false, 2, kRnHalf, 1, 1);
@@ -983,7 +983,7 @@ int rn_launch(RnParams& p, cudaStream_t st) {
   else if (s.pieces == 2)
     WP_RN(false, 2, 1024, 1, 1);
   else if (s.form == 1024) {
-    if constexpr (kBack) WP_RN(false, 1, 1024, 1, 1);   // forward such rows take two pieces
+    if constexpr (kBack && !kHalf) WP_RN(false, 1, 1024, 1, 1);   // others take two pieces a thread
   } else if (s.form == 640)
     WP_RN(false, 1, 640, 1, 1);
   else
