@@ -786,9 +786,11 @@ def lora_rope_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", s
         "linear"  every position divided by ``scale``
         "ntk"     the base raised by scale^(rot / (rot - 2)): the highest frequency kept, the lowest divided
         "yarn"    by parts: pairs that turn more than ``fast`` times in ``original_length`` positions kept,
-                  fewer than ``slow`` times divided by ``scale``, a ramp over i between; factor
+                  fewer than ``slow`` times divided by ``scale``, a ramp between; factor
                   0.1 ln(scale) + 1.
-    The ramp and factor are those of the YaRN method (Peng et al., 2023)."""
+    "yarn" is the method of Peng et al., 2023 with one difference: its text has the ramp linear in the turns that a pair
+    makes, its released models (so checkpoints) linear in the pair's index i, from the floor of the index that turns
+    ``fast`` times to the ceiling of the one that turns ``slow`` times.  This is the latter."""
     if rot <= 0 or rot % 2 or not (base > 0 and scale >= 1):
         raise ValueError("lora_rope_inv_freq: rot even and positive, base > 0, scale >= 1")
     i = torch.arange(rot // 2, dtype=torch.float64)
