@@ -541,14 +541,16 @@ int lora_rope(const wp_heads* Q, const wp_heads* K, const int32_t* positions, in
  *   loss[t] = lse[t] - z[t, target[t]]
  *   X [T, K], W [V, K] WP_BF16, K % 8 == 0, K <= 2^24, 16-byte aligned bases and pitches.
  *   target [T] int32 or int64 (target_bits 32 or 64) on the device.  A row whose target is outside
- *   0 .. V - 1 (-100 by convention) does not count: its loss and lse are 0, it costs nothing, and
- *   nothing in it, not even NaN, is read into another row's result.
+ *   0 .. V - 1 (-100 by convention) does not count: its loss and lse are 0, and nothing in it, not
+ *   even NaN, is read into another row's result.  Of more than 256 rows it costs nothing either; up to
+ *   256, W's one pass is the cost, whatever the rows.
  *   loss, lse [T] fp32; either may be NULL.
  *   workspace: lora_ce_workspace_size(X, W, 0) bytes, 16-byte aligned; the size for more rows serves
  *   fewer, too, and a larger one changes nothing.  (No two calls that may run at once may share one.)
  * Products are exact and summed in fp32: at most 1024 of them at a time on the tensor core, which cuts its sum every 16
  * products, and these sums with rounding to nearest: a logit is within about 2^-20 of its terms' magnitudes, and half a
- * step of fp32 for each further 1024 of K.
+ * step of fp32 for each further 1024 of K.  The same call gives the same bits; a row's last bits go by the number of rows,
+ * too, whose forms change at 16, 32, 64, 128 and 256.
  */
 int lora_ce_fwd(const wp_mat* X, const wp_mat* W, const void* target, int32_t target_bits, double logit_scale,
                 float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream);

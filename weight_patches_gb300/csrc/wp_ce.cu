@@ -19,7 +19,8 @@
 //
 // Rows that do not count (y_t outside the vocabulary) are left out: ce_pack_kernel copies the rows that
 // do next to each other first, and the products run over those alone, so an ignored row costs nothing and
-// nothing in it (not even NaN) reaches a gradient.  Their number stays on the device.
+// nothing in it (not even NaN) reaches a gradient.  Their number stays on the device.  (The loss of up to 256 rows has a
+// kernel of its own, ce_few_kernel, which computes them all.)
 #include <algorithm>
 #include <cmath>
 
