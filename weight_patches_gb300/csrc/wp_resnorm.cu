@@ -20,11 +20,11 @@
 // in the workers' order: no atomics, the same bits each time.
 //
 // Measured (device time; bytes read and written once over it; a copy of as many bytes runs at 6.7 TB/s):
-//   32760 x 1536, fp32 stream, bf16 block   forward 98.7 us, 6.1 TB/s; backward 148 us, 6.1 TB/s; with a post norm 103
-//                                           and 157
+//   32760 x 1536, fp32 stream, bf16 block   forward 100 us, 6.0 TB/s; backward 148 us, 6.1 TB/s; with a post norm 109
+//                                           and 156 (both without a mean; with means on both sides 117 and 158)
 //   32760 x 1536 bf16                       forward 68 us, 5.9 TB/s; backward 107 us, 5.7 TB/s
-//   16000 x 5120, fp32 stream               forward 153 us, 6.4 TB/s; backward 246 us, 6.0 TB/s
-//   20000 x 4096 bf16                       forward 106 us, 6.2 TB/s; backward 162 us, 6.1 TB/s
+//   16000 x 5120, fp32 stream               forward 152 us, 6.5 TB/s; backward 245 us, 6.0 TB/s
+//   20000 x 4096 bf16                       forward 107 us, 6.1 TB/s; backward 166 us, 5.9 TB/s
 //   100000 x 256 (a warp a row)             forward 58 us, 5.3 TB/s; backward 115 us, 4.0 TB/s
 //   4000 x 16384 bf16 (two pieces a thread) forward 224 us, 2.3 TB/s; backward 354 us, 2.2 TB/s: the forms spill
 //   8000 x 4099 bf16 (odd rows)             forward 83 us, 3.2 TB/s; backward 123 us, 3.2 TB/s: instructions
