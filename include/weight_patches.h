@@ -479,6 +479,7 @@ typedef struct wp_residual_norm {
  *   gate, post norm or X_out); X_out [T, C] of X's type or NULL (not wanted), X itself included; H [T, C] of
  *   Y's type.  Y and H are WP_BF16, or WP_FP32 with a WP_FP32 stream.
  *   stats [4, T] fp32 or NULL: mean and factor of norm2, then (rows 2 and 3, with a post norm only) of norm1.
+ *   Outputs overlap no input but for X_out in X's place.
  * C <= 16384, T < 2^30, any pitch; 16-byte aligned rows are fastest.  Sums are fp32, means taken out before squaring;
  * h is formed from x1 before its rounding to X_out's type; one rounding per output.  The order of a row's sums, and so
  * the last bits, go by the rows' length and types and by the addresses' and pitches' alignment, not by the rows' number; the
@@ -490,7 +491,8 @@ int lora_residual_norm_fwd(const wp_mat* X, const wp_mat* Y, const wp_residual_n
 /*
  * lora_residual_norm_bwd -- from dH at h and dX1 (NULL: zero) at the new stream, X1 and Y as the forward wrote
  * and read them, and its stats:
- *   dX [T, C] of X1's type (the gradient at x), dY [T, C] of dH's type; either may be NULL.  dX may be dX1.
+ *   dX [T, C] of X1's type (the gradient at x), dY [T, C] of dH's type; either may be NULL.  dX may be dX1; outputs overlap no
+ *   other input.
  *   dgate, dmul, dadd [n, C], dpost_weight [1, C]: WP_FP32, or NULL; overwritten (zero for no rows).  dgate, dmul
  *   and dpost_weight need their vector in `a`; of a->add only dadd's shape matters.
  *   workspace: lora_workspace_size(WP_OP_RESIDUAL_NORM_BWD, X1, NULL, NULL, 0) bytes, 16-byte aligned, when one of those
@@ -559,7 +561,8 @@ int lora_ce_fwd(const wp_mat* X, const wp_mat* W, const void* target, int32_t ta
  * lora_ce_bwd -- from the gradient dloss [T] fp32 at the rows' losses and the lse of lora_ce_fwd:
  *   G[t, v] = dloss[t] logit_scale (exp(z[t, v] - lse[t]) - [v = target[t]])   (0 in rows that do not count)
  *   dX = G W,   dW = G^T X
- *   dX [T, K], dW [V, K], WP_BF16 or WP_FP32, either NULL: not wanted; overwritten (dW of no rows: zeros).
+ *   dX [T, K], dW [V, K], WP_BF16 or WP_FP32, either NULL: not wanted; overwritten (dW of no rows: zeros).  They may not
+ *   overlap an input.
  * The logits are formed again, a piece of the vocabulary at a time; a row of G over its own 1 - p[target] is rounded
  * once to bf16 (the target's entry is then exact), whatever the outputs' types; sums are fp32, outputs are rounded once.
  * dX takes the row's factor, dloss (1 - p[target]), in fp32.  dW takes it times X, in two bf16 parts (2^-16 of it is left)
